@@ -30,7 +30,9 @@
  *    reserved (fd_reserve_workspace), no allocation, so they may be captured in a CUDA graph.
  *  - The library owns one grow-only device workspace per (device, stream) for its split plan and
  *    partial results, freed by fd_shutdown(). A call whose workspace must grow synchronises that
- *    stream once before reallocating.
+ *    stream once; the buffer it had stays allocated until fd_shutdown(), so graphs captured with it
+ *    may still be replayed. Calls captured on one stream share that stream's workspace: their
+ *    graphs must not run at the same time (capture them on streams of their own for that).
  *  - Errors: argument errors return before any launch (FD_ERR_INVALID_ARGUMENT /
  *    FD_ERR_UNSUPPORTED). CUDA errors map to FD_ERR_CUDA. fd_last_error_message() gives the
  *    detail for the calling thread. Nothing aborts or throws across the ABI.
@@ -86,6 +88,8 @@ typedef struct {
 #define FD_FLAG_WAIT_TIMEOUT 0x2u /* a kernel wait gave up; the call's results are invalid     */
 #define FD_FLAG_PLAN_OVERFLOW 0x4u /* the device plan exceeded the workspace bound (a bug)     */
 #define FD_FLAG_BAD_PAGE 0x8u      /* a block-table entry of a used page was outside the pool   */
+#define FD_FLAG_POOL_FULL 0x10u    /* a page operator ran out of free pages                    */
+#define FD_FLAG_BAD_INDEX 0x20u    /* a page operator met an invalid sequence index or keep list */
 
 /*
  * fd_decode_attention — split-KV FlashDecoding decode attention (one query token per sequence).
@@ -301,6 +305,185 @@ fd_status fd_decode_attention_static(const fd_tensor* q, const fd_tensor* k_cach
                                      const fd_tensor* v_cache, const int32_t* cache_lens,
                                      int32_t num_splits, fd_tensor* out, float* lse,
                                      void* stream);
+
+/*
+ * fd_prompt_attention — causal attention of whole prompts, packed one after another.
+ *
+ * The pages attend to a cache only; this call is the pass over a prompt whose keys and values are
+ * still the projection's output: request b holds the rows [start_b, start_b + seq_lens[b]) of all
+ * tensors, start_b = seq_lens[0] + ... + seq_lens[b-1], and its row i sees its rows j <= i:
+ *
+ *   out[start_b+i,h,:] = sum_{j<=i} softmax_j(q[start_b+i,h,:]·k[start_b+j,kv,:] / sqrt(D)) · v[start_b+j,kv,:]
+ *
+ *  q         [T, Hq, D]   FD_BF16, D in {64, 128}, Hq / Hkv <= 16.
+ *  k, v      [T, Hkv, D]  FD_BF16. Rows and heads may have any strides that are multiples of 16
+ *                         bytes (slices of one fused projection, say), each tensor its own; data
+ *                         16-byte aligned.
+ *  seq_lens  [batch] int32 (device), each >= 0 (a negative one counts as 0, status flag). Rows
+ *            behind the last request (sum(seq_lens) < T: a batch padded for a captured graph) are
+ *            neither read into a result nor written. If the lengths sum to more than T nothing is
+ *            computed, out and lse are left unchanged and FD_FLAG_LEN_CLAMPED is raised.
+ *  out       [T, Hq, D]   FD_BF16 (written); lse [T, Hq] float32 (contiguous, written, natural
+ *            log).
+ * v must be finite in the rows of a request (a non-finite value may reach the request's other
+ * rows); other rows may hold anything. out must not overlap q, k or v.
+ */
+fd_status fd_prompt_attention(const fd_tensor* q, const fd_tensor* k, const fd_tensor* v,
+                              const int32_t* seq_lens, int32_t batch, fd_tensor* out, float* lse,
+                              void* stream);
+
+/* Device workspace bytes a prompt call of this shape needs (any lengths). */
+size_t fd_prompt_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_q_heads,
+                                 int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * fd_tree_attention — attention of drafted token trees over a cache (tree verification).
+ *
+ * FlashDecoding page, "与其他推理加速方案的组合使用", item "Speculative Decoding + FlashDecoding",
+ * checks k drafted tokens in one pass; the drafts of fd_chunk_prefill_attention form one line, here
+ * they form a tree: the drafts of request b are the rows [start_b, start_b + tree_lens[b]) of q
+ * (start_b the sum of the lengths before), their keys and values stand in the cache at
+ * [prefix_lens[b], prefix_lens[b] + tree_lens[b]), and draft i sees every key of the prefix and the
+ * drafts j whose bit is set in its row of the mask: bit j % 32 of tree_mask[start_b + i][j / 32].
+ * A draft sees itself only if its own bit is set; bits j >= tree_lens[b] are ignored. A row that
+ * sees no key gives out = 0 and lse = -inf.
+ *
+ *  q            [T, Hq, D] FD_BF16, D in {64, 128}, Hq / Hkv <= 16.
+ *  k_cache,     [B, Hkv, S_cap, D] FD_BF16; layout rules of fd_decode_attention.
+ *  v_cache
+ *  prefix_lens, tree_lens  [B] int32 (device). prefix is clamped into [0, S_cap]; drafts behind
+ *               S_cap are not seen (status flag for both). If a tree length is negative or above
+ *               32 * mask_words, or the lengths sum to more than T, nothing is computed, out and
+ *               lse are left unchanged and FD_FLAG_LEN_CLAMPED is raised. Rows behind the last
+ *               request are left unchanged.
+ *  tree_mask    [T][mask_words] 32-bit words (device, contiguous), 1 <= mask_words <= 8.
+ *  out, lse     as in fd_prompt_attention.
+ * v must be finite at a request's keys [0, prefix + tree_len); what stands behind may be anything.
+ */
+fd_status fd_tree_attention(const fd_tensor* q, const fd_tensor* k_cache, const fd_tensor* v_cache,
+                            const int32_t* prefix_lens, const int32_t* tree_lens,
+                            const int32_t* tree_mask, int32_t mask_words, fd_tensor* out,
+                            float* lse, void* stream);
+
+/* fd_tree_attention over a paged cache: pages and block table as in fd_decode_attention_paged,
+ * `batch` rows in the block table. S_cap is pages_per_seq * page_size. */
+fd_status fd_tree_attention_paged(const fd_tensor* q, const fd_tensor* k_pages,
+                                  const fd_tensor* v_pages, const int32_t* block_table,
+                                  int32_t pages_per_seq, int32_t batch,
+                                  const int32_t* prefix_lens, const int32_t* tree_lens,
+                                  const int32_t* tree_mask, int32_t mask_words, fd_tensor* out,
+                                  float* lse, void* stream);
+
+/* Device workspace bytes a tree call of this shape needs (any lengths and masks). */
+size_t fd_tree_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t cache_capacity, int32_t head_dim);
+
+/*
+ * The operators of a paged cache's pages.
+ *
+ * FlashDecoding page, "部署落地的工程细节", pairs split-KV decoding with a paged cache and names no
+ * layout; these calls keep the block-table form of fd_decode_attention_paged. All of its state is
+ * the caller's device memory:
+ *  k_pages, v_pages [num_pages, Hkv, page_size, D] as in fd_decode_attention_paged;
+ *  block_table      [batch][pages_per_seq] int32: the pages of a sequence are the leading
+ *                   non-negative entries of its row (what stands behind the first negative entry
+ *                   is ignored); an empty row starts with a negative entry;
+ *  page_refs        [num_pages] int32: in how many rows a page stands; 0 is a free page;
+ *  cache_lens       [batch] int32.
+ * New pages are taken lowest index first, in the order of the sequences (of the pairs, in
+ * fd_pages_fork), so that results are reproducible. batch and the lists' counts are at most 4096.
+ * The calls are asynchronous, take no host copy of any of this state, and may be captured. Two calls
+ * on the same state must be ordered by the caller.
+ * Flags raised (fd_poll_status): FD_FLAG_BAD_PAGE for an entry outside the pool or a page whose
+ * references do not allow the call, FD_FLAG_BAD_INDEX for a sequence index or a keep list that is
+ * not valid, FD_FLAG_POOL_FULL when pages ran out, FD_FLAG_LEN_CLAMPED for lengths beyond a row's
+ * capacity. What a flag reports is skipped, as each call describes; nothing else is affected.
+ */
+
+/*
+ * fd_pages_append — write new tokens' keys and values into the pages of their sequences.
+ *
+ * Token i of sequence b is packed row start_b + i (start_b the sum of new_lens before b) of
+ *  k_new, v_new [T, Hkv, D]  the pages' dtype (FD_F32 or FD_BF16); any strides that are multiples
+ *               of 16 bytes, each tensor its own
+ * and goes to position start_lens[b] + i of the sequence, whose pages must stand in its row and
+ * belong to it alone there (fd_pages_reserve gives them). cache_lens is not involved.
+ *  start_lens, new_lens [batch] int32 (device). A negative new_lens counts as 0, a negative start
+ *               skips its sequence, positions beyond the row's capacity are not written
+ *               (FD_FLAG_LEN_CLAMPED); a position whose entry is outside the pool is not written
+ *               (FD_FLAG_BAD_PAGE). If new_lens sum to more than T nothing is written
+ *               (FD_FLAG_LEN_CLAMPED); rows behind the last sequence are not read.
+ */
+fd_status fd_pages_append(const fd_tensor* k_new, const fd_tensor* v_new, fd_tensor* k_pages,
+                          fd_tensor* v_pages, const int32_t* block_table, int32_t pages_per_seq,
+                          int32_t batch, const int32_t* start_lens, const int32_t* new_lens,
+                          void* stream);
+
+/* fd_pages_append into FD_E4M3 pages: k_new, v_new are FD_BF16 or FD_F32, and the code of x is the
+ * E4M3 value nearest to x / scale (ties to even; beyond +-448, infinities included, the code of
+ * +-448; NaN gives a NaN code). k_scale, v_scale finite, > 0. */
+fd_status fd_pages_append_fp8(const fd_tensor* k_new, const fd_tensor* v_new, fd_tensor* k_pages,
+                              fd_tensor* v_pages, float k_scale, float v_scale,
+                              const int32_t* block_table, int32_t pages_per_seq, int32_t batch,
+                              const int32_t* start_lens, const int32_t* new_lens, void* stream);
+
+/*
+ * fd_pages_reserve — give every sequence the pages for want_lens[b] tokens.
+ *
+ * A sequence with fewer than ceil(want_lens[b] / page_size) pages gets the missing ones (references
+ * 1). Sequences are served in order while the free pages last: the first one whose missing pages are
+ * not all there, and every later one that misses any, get none (FD_FLAG_POOL_FULL). A want beyond
+ * the row's capacity counts as the capacity (FD_FLAG_LEN_CLAMPED).
+ */
+fd_status fd_pages_reserve(int32_t* page_refs, int32_t num_pages, int32_t* block_table,
+                           int32_t pages_per_seq, int32_t batch, const int32_t* want_lens,
+                           int32_t page_size, void* stream);
+
+/*
+ * fd_pages_fork — make dst_seqs[i] a copy of src_seqs[i], i < count (device lists).
+ *
+ * With n = cache_lens[src]: the full pages [0, n / page_size) are shared (one more reference each),
+ * the n % page_size rows of the last one are copied to a new page, the rest of dst's row becomes -1
+ * and cache_lens[dst] = n. Sources are read as they stood before the call. A pair is skipped, dst
+ * left as it was, when an index is outside [0, batch), dst's row is not empty or dst stands earlier
+ * in the list (FD_FLAG_BAD_INDEX), when src lacks pages for n tokens, or one lies outside the pool or has no
+ * reference (FD_FLAG_BAD_PAGE), or when, in the order of the pairs, the free pages run out as in
+ * fd_pages_reserve (FD_FLAG_POOL_FULL).
+ */
+fd_status fd_pages_fork(fd_tensor* k_pages, fd_tensor* v_pages, int32_t* page_refs,
+                        int32_t* block_table, int32_t pages_per_seq, int32_t batch,
+                        int32_t* cache_lens, const int32_t* src_seqs, const int32_t* dst_seqs,
+                        int32_t count, void* stream);
+
+/*
+ * fd_pages_free — empty the rows of seqs[i], i < count (device list): one reference less for each of
+ * their pages, entries -1, cache_lens 0. An index that stands twice is freed once; one outside
+ * [0, batch) is skipped (FD_FLAG_BAD_INDEX). A page outside the pool, or without a reference to
+ * give up, is only taken out of the row (FD_FLAG_BAD_PAGE).
+ */
+fd_status fd_pages_free(int32_t* page_refs, int32_t num_pages, int32_t* block_table,
+                        int32_t pages_per_seq, int32_t batch, int32_t* cache_lens,
+                        const int32_t* seqs, int32_t count, void* stream);
+
+/*
+ * fd_pages_compact — keep some of a sequence's tokens, close the gaps, give the rest's pages back.
+ *
+ * For every sequence b with keep_lens[b] >= 0: the token at position start_lens[b] + keep[b][i] moves
+ * to position start_lens[b] + i, i < keep_lens[b]; cache_lens[b] becomes start_lens[b] + keep_lens[b]
+ * and the pages behind that length are given back (one reference less, entries -1). The accepted
+ * path of a verified tree, or the tokens that an eviction rule keeps. keep_lens[b] < 0 leaves the
+ * sequence as it is.
+ *  keep       [batch][max_keep] int32 (device, contiguous): offsets, strictly increasing, >= 0.
+ *  keep_lens  [batch] int32, at most max_keep.
+ * A sequence is left as it is when its list breaks these rules or its start is negative
+ * (FD_FLAG_BAD_INDEX), or when, between the first position that changes and the last one kept, a page
+ * is missing or outside the pool, or one whose rows would change does not have exactly one reference
+ * (FD_FLAG_BAD_PAGE); references are read as they stood before the call.
+ */
+fd_status fd_pages_compact(fd_tensor* k_pages, fd_tensor* v_pages, int32_t* page_refs,
+                           int32_t* block_table, int32_t pages_per_seq, int32_t batch,
+                           int32_t* cache_lens, const int32_t* start_lens, const int32_t* keep,
+                           int32_t max_keep, const int32_t* keep_lens, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* fd_status_string(fd_status s);

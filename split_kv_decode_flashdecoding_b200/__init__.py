@@ -11,6 +11,11 @@ Functions keep the C names:
 * ``fd_chunk_prefill_attention(q_chunk, k_cache, v_cache, prefix_lens, chunk_lens, out=None, lse=None)``
 * ``fd_split_plan(cache_lens, num_kv_heads, cache_capacity, num_splits=0, num_ctas=148)``
 * ``fd_split_plan_device(cache_lens, num_kv_heads, cache_capacity, num_splits=0, num_ctas=148)``
+* ``fd_prompt_attention(q, k, v, seq_lens, out=None, lse=None)``
+* ``fd_tree_attention(q, k_cache, v_cache, prefix_lens, tree_lens, tree_mask, out=None, lse=None)``
+  and ``fd_tree_attention_paged``
+* ``fd_pages_reserve``, ``fd_pages_append``, ``fd_pages_append_fp8``, ``fd_pages_fork``,
+  ``fd_pages_compact``, ``fd_pages_free`` on a paged cache's device state
 * status, workspace and profiling helpers.
 """
 
@@ -30,6 +35,10 @@ __all__ = [
     "fd_chunk_workspace_bytes", "fd_reserve_workspace", "fd_poll_status", "fd_profile_begin",
     "fd_profile_end", "fd_shutdown", "fd_status_string", "FD_F32", "FD_BF16", "FD_E4M3",
     "FD_FLAG_LEN_CLAMPED", "FD_FLAG_WAIT_TIMEOUT", "FD_FLAG_PLAN_OVERFLOW", "FD_FLAG_BAD_PAGE",
+    "fd_prompt_attention", "fd_prompt_workspace_bytes", "fd_tree_attention",
+    "fd_tree_attention_paged", "fd_tree_workspace_bytes", "fd_pages_append",
+    "fd_pages_append_fp8", "fd_pages_reserve", "fd_pages_fork", "fd_pages_free",
+    "fd_pages_compact", "FD_FLAG_POOL_FULL", "FD_FLAG_BAD_INDEX",
     "ABI_FUNCTIONS",
 ]
 
@@ -41,6 +50,8 @@ FD_FLAG_LEN_CLAMPED = 0x1
 FD_FLAG_WAIT_TIMEOUT = 0x2
 FD_FLAG_PLAN_OVERFLOW = 0x4
 FD_FLAG_BAD_PAGE = 0x8
+FD_FLAG_POOL_FULL = 0x10
+FD_FLAG_BAD_INDEX = 0x20
 
 c_i32, c_i64, c_size, c_vp, c_f32p = (ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t,
                                       ctypes.c_void_p, ctypes.POINTER(ctypes.c_float))
@@ -86,6 +97,22 @@ ABI_FUNCTIONS = {
                                         c_i32, _TP, c_f32p, c_vp]),
     "fd_decode_attention_paged_fp8": (c_i32, [_TP, _TP, _TP, ctypes.c_float, ctypes.c_float,
                                               c_i32p, c_i32, c_i32p, c_i32, _TP, c_f32p, c_vp]),
+    "fd_prompt_attention": (c_i32, [_TP, _TP, _TP, c_i32p, c_i32, _TP, c_f32p, c_vp]),
+    "fd_prompt_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "fd_tree_attention": (c_i32, [_TP, _TP, _TP, c_i32p, c_i32p, c_i32p, c_i32, _TP, c_f32p,
+                                  c_vp]),
+    "fd_tree_attention_paged": (c_i32, [_TP, _TP, _TP, c_i32p, c_i32, c_i32, c_i32p, c_i32p,
+                                        c_i32p, c_i32, _TP, c_f32p, c_vp]),
+    "fd_tree_workspace_bytes": (c_size, [c_i32, c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "fd_pages_append": (c_i32, [_TP, _TP, _TP, _TP, c_i32p, c_i32, c_i32, c_i32p, c_i32p, c_vp]),
+    "fd_pages_append_fp8": (c_i32, [_TP, _TP, _TP, _TP, ctypes.c_float, ctypes.c_float, c_i32p,
+                                    c_i32, c_i32, c_i32p, c_i32p, c_vp]),
+    "fd_pages_reserve": (c_i32, [c_i32p, c_i32, c_i32p, c_i32, c_i32, c_i32p, c_i32, c_vp]),
+    "fd_pages_fork": (c_i32, [_TP, _TP, c_i32p, c_i32p, c_i32, c_i32, c_i32p, c_i32p, c_i32p,
+                              c_i32, c_vp]),
+    "fd_pages_free": (c_i32, [c_i32p, c_i32, c_i32p, c_i32, c_i32, c_i32p, c_i32p, c_i32, c_vp]),
+    "fd_pages_compact": (c_i32, [_TP, _TP, c_i32p, c_i32p, c_i32, c_i32, c_i32p, c_i32p, c_i32p,
+                                 c_i32, c_i32p, c_vp]),
     "fd_status_string": (ctypes.c_char_p, [c_i32]),
     "fd_last_error_message": (ctypes.c_char_p, []),
     "fd_decode_num_ctas": (c_i32, [c_i32, c_i32, c_i32, c_i32]),
@@ -264,6 +291,213 @@ def fd_chunk_prefill_attention(q_chunk: torch.Tensor, k_cache: torch.Tensor,
             _stream(stream, q_chunk.device))
     _check(st, "fd_chunk_prefill_attention")
     return out, lse
+
+
+def _int32(t: torch.Tensor, name: str, like: torch.Tensor, *shape: int) -> ctypes.c_void_p:
+    """Pointer of a contiguous int32 tensor of this shape (-1: any size) on like's device."""
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.device != like.device or \
+            t.dim() != len(shape) or any(n >= 0 and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a contiguous int32 tensor "
+                         f"[{', '.join('*' if n < 0 else str(n) for n in shape)}] on {like.device}")
+    return _ptr(t, c_i32)
+
+
+def _rows_out(q: torch.Tensor, out, lse):
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if lse is None:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != q.shape[:2]:
+        raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
+    return out, lse
+
+
+def _same_device(like: torch.Tensor, **tensors: torch.Tensor) -> None:
+    for name, t in tensors.items():
+        if t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def fd_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor,
+                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention of whole prompts packed one after another. q [T,Hq,D]; k, v [T,Hkv,D] (bf16,
+    any 16-byte strides of rows and heads); seq_lens int32 [B], summing to at most T. Rows behind
+    the last prompt are left as they are. Returns (out [T,Hq,D], lse float32 [T,Hq])."""
+    out, lse = _rows_out(q, out, lse)
+    _same_device(q, k=k, v=v, out=out, lse=lse)
+    lens = _int32(seq_lens, "seq_lens", q, -1)
+    with torch.cuda.device(q.device):
+        st = lib.fd_prompt_attention(ctypes.byref(_tensor(q)), ctypes.byref(_tensor(k)),
+                                     ctypes.byref(_tensor(v)), lens, seq_lens.numel(),
+                                     ctypes.byref(_tensor(out)), _ptr(lse, ctypes.c_float),
+                                     _stream(stream, q.device))
+    _check(st, "fd_prompt_attention")
+    return out, lse
+
+
+def fd_prompt_workspace_bytes(batch, total_rows, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(lib.fd_prompt_workspace_bytes(batch, total_rows, num_q_heads, num_kv_heads,
+                                             head_dim))
+
+
+def fd_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      prefix_lens: torch.Tensor, tree_lens: torch.Tensor, tree_mask: torch.Tensor,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of drafted token trees over a cache. q [T,Hq,D] packs tree_lens[b] drafts a request,
+    whose keys and values stand in the cache at [prefix_lens[b], prefix_lens[b] + tree_lens[b]);
+    draft i sees the prefix and the drafts j with bit j % 32 of tree_mask[row][j // 32] set
+    (tree_mask int32 [T, W], W <= 8)."""
+    out, lse = _rows_out(q, out, lse)
+    _same_device(q, k_cache=k_cache, v_cache=v_cache, out=out, lse=lse)
+    B = k_cache.shape[0]
+    pre, new = _int32(prefix_lens, "prefix_lens", q, B), _int32(tree_lens, "tree_lens", q, B)
+    mask = _int32(tree_mask, "tree_mask", q, q.shape[0], -1)
+    with torch.cuda.device(q.device):
+        st = lib.fd_tree_attention(ctypes.byref(_tensor(q)), ctypes.byref(_tensor(k_cache)),
+                                   ctypes.byref(_tensor(v_cache)), pre, new, mask,
+                                   tree_mask.shape[1], ctypes.byref(_tensor(out)),
+                                   _ptr(lse, ctypes.c_float), _stream(stream, q.device))
+    _check(st, "fd_tree_attention")
+    return out, lse
+
+
+def fd_tree_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                            block_table: torch.Tensor, prefix_lens: torch.Tensor,
+                            tree_lens: torch.Tensor, tree_mask: torch.Tensor,
+                            out: Optional[torch.Tensor] = None,
+                            lse: Optional[torch.Tensor] = None,
+                            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """fd_tree_attention over a paged cache (pages and block_table as in
+    fd_decode_attention_paged)."""
+    out, lse = _rows_out(q, out, lse)
+    _same_device(q, k_pages=k_pages, v_pages=v_pages, out=out, lse=lse)
+    table = _int32(block_table, "block_table", q, -1, -1)
+    B = block_table.shape[0]
+    pre, new = _int32(prefix_lens, "prefix_lens", q, B), _int32(tree_lens, "tree_lens", q, B)
+    mask = _int32(tree_mask, "tree_mask", q, q.shape[0], -1)
+    with torch.cuda.device(q.device):
+        st = lib.fd_tree_attention_paged(
+            ctypes.byref(_tensor(q)), ctypes.byref(_tensor(k_pages)),
+            ctypes.byref(_tensor(v_pages)), table, block_table.shape[1], B, pre, new, mask,
+            tree_mask.shape[1], ctypes.byref(_tensor(out)), _ptr(lse, ctypes.c_float),
+            _stream(stream, q.device))
+    _check(st, "fd_tree_attention_paged")
+    return out, lse
+
+
+def fd_tree_workspace_bytes(batch, total_rows, num_q_heads, num_kv_heads, cache_capacity,
+                            head_dim) -> int:
+    return int(lib.fd_tree_workspace_bytes(batch, total_rows, num_q_heads, num_kv_heads,
+                                           cache_capacity, head_dim))
+
+
+def fd_pages_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                    v_pages: torch.Tensor, block_table: torch.Tensor, start_lens: torch.Tensor,
+                    new_lens: torch.Tensor, stream=None) -> None:
+    """Write the packed rows k_new, v_new [T,Hkv,D] (new_lens[b] rows a sequence) to the positions
+    start_lens[b], start_lens[b] + 1, ... of their sequences' pages (in place)."""
+    _same_device(k_pages, k_new=k_new, v_new=v_new, v_pages=v_pages)
+    table = _int32(block_table, "block_table", k_pages, -1, -1)
+    B = block_table.shape[0]
+    start = _int32(start_lens, "start_lens", k_pages, B)
+    new = _int32(new_lens, "new_lens", k_pages, B)
+    with torch.cuda.device(k_pages.device):
+        st = lib.fd_pages_append(ctypes.byref(_tensor(k_new)), ctypes.byref(_tensor(v_new)),
+                                 ctypes.byref(_tensor(k_pages)), ctypes.byref(_tensor(v_pages)),
+                                 table, block_table.shape[1], B, start, new,
+                                 _stream(stream, k_pages.device))
+    _check(st, "fd_pages_append")
+
+
+def fd_pages_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
+                        v_pages: torch.Tensor, k_scale: float, v_scale: float,
+                        block_table: torch.Tensor, start_lens: torch.Tensor,
+                        new_lens: torch.Tensor, stream=None) -> None:
+    """fd_pages_append into E4M3 pages (float8_e4m3fn, or uint8 codes): the code of x is the E4M3
+    value nearest to x / scale."""
+    _same_device(k_pages, k_new=k_new, v_new=v_new, v_pages=v_pages)
+    table = _int32(block_table, "block_table", k_pages, -1, -1)
+    B = block_table.shape[0]
+    start = _int32(start_lens, "start_lens", k_pages, B)
+    new = _int32(new_lens, "new_lens", k_pages, B)
+    with torch.cuda.device(k_pages.device):
+        st = lib.fd_pages_append_fp8(ctypes.byref(_tensor(k_new)), ctypes.byref(_tensor(v_new)),
+                                     ctypes.byref(_tensor(k_pages)),
+                                     ctypes.byref(_tensor(v_pages)), float(k_scale),
+                                     float(v_scale), table, block_table.shape[1], B, start, new,
+                                     _stream(stream, k_pages.device))
+    _check(st, "fd_pages_append_fp8")
+
+
+def fd_pages_reserve(page_refs: torch.Tensor, block_table: torch.Tensor, want_lens: torch.Tensor,
+                     page_size: int, stream=None) -> None:
+    """Give every sequence the pages for want_lens[b] tokens: free ones (page_refs 0), lowest
+    index first, in the order of the sequences (block_table and page_refs in place)."""
+    refs = _int32(page_refs, "page_refs", page_refs, -1)
+    table = _int32(block_table, "block_table", page_refs, -1, -1)
+    B = block_table.shape[0]
+    want = _int32(want_lens, "want_lens", page_refs, B)
+    with torch.cuda.device(page_refs.device):
+        st = lib.fd_pages_reserve(refs, page_refs.numel(), table, block_table.shape[1], B, want,
+                                  int(page_size), _stream(stream, page_refs.device))
+    _check(st, "fd_pages_reserve")
+
+
+def fd_pages_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_refs: torch.Tensor,
+                  block_table: torch.Tensor, cache_lens: torch.Tensor, src_seqs: torch.Tensor,
+                  dst_seqs: torch.Tensor, stream=None) -> None:
+    """Make the empty sequence dst_seqs[i] a copy of src_seqs[i]: full pages are shared, the rows
+    of a last, partly filled page are copied to a new page (all state in place)."""
+    _same_device(k_pages, v_pages=v_pages)
+    refs = _int32(page_refs, "page_refs", k_pages, k_pages.shape[0])
+    table = _int32(block_table, "block_table", k_pages, -1, -1)
+    B = block_table.shape[0]
+    lens = _int32(cache_lens, "cache_lens", k_pages, B)
+    src = _int32(src_seqs, "src_seqs", k_pages, -1)
+    dst = _int32(dst_seqs, "dst_seqs", k_pages, src_seqs.numel())
+    with torch.cuda.device(k_pages.device):
+        st = lib.fd_pages_fork(ctypes.byref(_tensor(k_pages)), ctypes.byref(_tensor(v_pages)), refs,
+                               table, block_table.shape[1], B, lens, src, dst, src_seqs.numel(),
+                               _stream(stream, k_pages.device))
+    _check(st, "fd_pages_fork")
+
+
+def fd_pages_free(page_refs: torch.Tensor, block_table: torch.Tensor, cache_lens: torch.Tensor,
+                  seqs: torch.Tensor, stream=None) -> None:
+    """Empty the rows of the listed sequences and give their references back (in place)."""
+    refs = _int32(page_refs, "page_refs", page_refs, -1)
+    table = _int32(block_table, "block_table", page_refs, -1, -1)
+    B = block_table.shape[0]
+    lens = _int32(cache_lens, "cache_lens", page_refs, B)
+    ids = _int32(seqs, "seqs", page_refs, -1)
+    with torch.cuda.device(page_refs.device):
+        st = lib.fd_pages_free(refs, page_refs.numel(), table, block_table.shape[1], B, lens, ids,
+                               seqs.numel(), _stream(stream, page_refs.device))
+    _check(st, "fd_pages_free")
+
+
+def fd_pages_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_refs: torch.Tensor,
+                     block_table: torch.Tensor, cache_lens: torch.Tensor,
+                     start_lens: torch.Tensor, keep: torch.Tensor, keep_lens: torch.Tensor,
+                     stream=None) -> None:
+    """Keep the tokens start_lens[b] + keep[b, :keep_lens[b]] of every sequence with keep_lens[b] >= 0,
+    moved to start_lens[b], start_lens[b] + 1, ...; cache_lens and the pages follow (in place).
+    keep int32 [B, max_keep], strictly increasing rows."""
+    _same_device(k_pages, v_pages=v_pages)
+    refs = _int32(page_refs, "page_refs", k_pages, k_pages.shape[0])
+    table = _int32(block_table, "block_table", k_pages, -1, -1)
+    B = block_table.shape[0]
+    lens = _int32(cache_lens, "cache_lens", k_pages, B)
+    start = _int32(start_lens, "start_lens", k_pages, B)
+    kept = _int32(keep_lens, "keep_lens", k_pages, B)
+    lists = _int32(keep, "keep", k_pages, B, -1)
+    with torch.cuda.device(k_pages.device):
+        st = lib.fd_pages_compact(ctypes.byref(_tensor(k_pages)), ctypes.byref(_tensor(v_pages)),
+                                  refs, table, block_table.shape[1], B, lens, start, lists,
+                                  keep.shape[1], kept, _stream(stream, k_pages.device))
+    _check(st, "fd_pages_compact")
 
 
 def fd_split_plan(cache_lens: Sequence[int], num_kv_heads: int, cache_capacity: int,

@@ -15,6 +15,19 @@ namespace fd_abi {
 fd_status fail(fd_status s, const char* fmt, ...);
 fd_status cuda_fail(cudaError_t e, const char* what);
 
+// Device workspace of (current device, `stream`): at least `need` bytes, grown when the stream is
+// not being captured. `view` (may be nullptr) also gets the stream's side stream and events.
+struct Workspace;
+fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace* view);
+
+int sm_count(int dev);
+
+// A tensor of `ndim` dimensions with a known dtype, sizes in int32, contiguous last dimension.
+fd_status check_tensor(const fd_tensor* t, const char* name, int ndim);
+size_t elem_size(int dtype);
+bool aligned16(const void* p);
+bool stride16(int64_t stride_elems, int dtype);
+
 struct DecodeShape {
   int B, hq, hkv, g, d, cap, dtype;
   bool use_tc;

@@ -53,13 +53,14 @@ fd_status cuda_fail(cudaError_t e, const char* what) {
 struct Workspace {
   void* ptr = nullptr;
   size_t bytes = 0;
+  std::vector<void*> outgrown;  // smaller buffers it replaced, freed by fd_shutdown
   cudaStream_t side = nullptr;
   cudaEvent_t fork = nullptr, join = nullptr;
 };
 std::mutex g_mu;
 std::map<std::pair<int, uintptr_t>, Workspace> g_ws;
 
-fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace* view = nullptr) {
+fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace* view) {
   int dev = 0;
   FD_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   std::lock_guard<std::mutex> lock(g_mu);
@@ -76,18 +77,18 @@ fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace*
                 "workspace of this stream holds %zu bytes but the call needs %zu; reserve it with "
                 "fd_reserve_workspace before capturing",
                 w.bytes, need);
-  uint32_t old_status = 0;
-  if (w.ptr) {
-    FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
-    FD_CUDA(cudaMemcpy(&old_status, w.ptr, sizeof(uint32_t), cudaMemcpyDeviceToHost), "read status");
-    FD_CUDA(cudaFree(w.ptr), "cudaFree(workspace)");
-    w.ptr = nullptr;
-    w.bytes = 0;
-  }
-  size_t nb = std::max(need, static_cast<size_t>(1) << 20);
-  nb = (nb + (2u << 20) - 1) / (2u << 20) * (2u << 20);
+  // A buffer that is outgrown stays allocated until fd_shutdown: graphs captured with it may still
+  // be replayed. A new one is twice as large where memory allows it, so that what is kept stays
+  // below the current one's size.
+  const auto rounded = [](size_t n) { return (n + (2u << 20) - 1) / (2u << 20) * (2u << 20); };
+  size_t nb = rounded(std::max({need, static_cast<size_t>(1) << 20, 2 * w.bytes}));
   void* p = nullptr;
   cudaError_t e = cudaMalloc(&p, nb);
+  if (e != cudaSuccess && rounded(need) < nb) {
+    (void)cudaGetLastError();
+    nb = rounded(need);
+    e = cudaMalloc(&p, nb);
+  }
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return fail(FD_ERR_WORKSPACE, "cudaMalloc of %zu workspace bytes failed: %s", nb,
@@ -95,9 +96,9 @@ fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace*
   }
   WsHeader h;
   std::memset(&h, 0, sizeof(h));
-  h.status = old_status;
   FD_CUDA(cudaMemcpyAsync(p, &h, sizeof(h), cudaMemcpyHostToDevice, stream), "init workspace");
   FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
+  if (w.ptr) w.outgrown.push_back(w.ptr);
   w.ptr = p;
   w.bytes = nb;
   if (!w.side) {
@@ -498,7 +499,7 @@ fd_status fd_split_plan_device(const int32_t* cache_lens, int32_t batch, int32_t
   const int64_t items = decode_max_items(batch, num_kv_heads, cache_capacity, num_splits, num_ctas);
   const WsLayout L = ws_layout(items, 0, batch, 0, 1, 1, num_kv_heads);
   void* ws = nullptr;
-  fd_status s = get_workspace(stream, L.total, &ws);
+  fd_status s = get_workspace(stream, L.total, &ws, nullptr);
   if (s != FD_OK) return s;
   char* base = static_cast<char*>(ws);
   PlanParams pp{};
@@ -558,7 +559,7 @@ fd_status decode_call(const fd_tensor* q, const fd_tensor* k_cache, const fd_ten
                   "the %s; use fd_decode_attention",
                   L.total, preset->bytes, preset->name);
     ws = preset->base;
-  } else if ((s = get_workspace(stream, L.total, &ws)) != FD_OK) {
+  } else if ((s = get_workspace(stream, L.total, &ws, nullptr)) != FD_OK) {
     return s;
   }
   char* base = static_cast<char*>(ws);
@@ -990,7 +991,7 @@ size_t fd_chunk_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_q
 
 fd_status fd_reserve_workspace(size_t bytes, void* stream_) {
   void* ws = nullptr;
-  return get_workspace(static_cast<cudaStream_t>(stream_), std::max(bytes, sizeof(WsHeader)), &ws);
+  return get_workspace(static_cast<cudaStream_t>(stream_), std::max(bytes, sizeof(WsHeader)), &ws, nullptr);
 }
 
 fd_status fd_poll_status(void* stream_, uint32_t* flags) {
@@ -1000,17 +1001,22 @@ fd_status fd_poll_status(void* stream_, uint32_t* flags) {
   int dev = 0;
   FD_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
-  void* ptr = nullptr;
+  std::vector<void*> buffers;  // the stream's workspace and those it has outgrown
   {
     std::lock_guard<std::mutex> lock(g_mu);
     auto it = g_ws.find({dev, reinterpret_cast<uintptr_t>(stream)});
-    if (it != g_ws.end()) ptr = it->second.ptr;
+    if (it != g_ws.end() && it->second.ptr) {
+      buffers = it->second.outgrown;
+      buffers.push_back(it->second.ptr);
+    }
   }
   uint32_t v = 0;
-  if (ptr) {
-    FD_CUDA(cudaMemcpy(&v, ptr, sizeof(v), cudaMemcpyDeviceToHost), "read status");
+  for (void* ptr : buffers) {
+    uint32_t one = 0;
+    FD_CUDA(cudaMemcpy(&one, ptr, sizeof(one), cudaMemcpyDeviceToHost), "read status");
     const uint32_t zero = 0;
     FD_CUDA(cudaMemcpy(ptr, &zero, sizeof(zero), cudaMemcpyHostToDevice), "clear status");
+    v |= one;
   }
   // the status bits of fd_decode_attention_static calls on this device
   uint32_t st = 0;
@@ -1061,6 +1067,7 @@ void fd_shutdown(void) {
       cudaSetDevice(kv.first.first);
       cudaDeviceSynchronize();
       if (kv.second.ptr) cudaFree(kv.second.ptr);
+      for (void* ptr : kv.second.outgrown) cudaFree(ptr);
       if (kv.second.side) cudaStreamDestroy(kv.second.side);
       if (kv.second.fork) cudaEventDestroy(kv.second.fork);
       if (kv.second.join) cudaEventDestroy(kv.second.join);

@@ -1,0 +1,600 @@
+// Operators of a paged cache's pages: appending new tokens, reserving, forking and freeing pages,
+// compacting a sequence's tokens. Layout as in fd_decode_attention_paged: pools
+// [num_pages, Hkv, page_size, D] read through a block table [batch, pages_per_seq] (FlashDecoding
+// page, "部署落地的工程细节", names a paged cache without a layout).
+#include <cfloat>
+
+#include "abi_internal.h"
+#include "common.cuh"
+#include "pages.h"
+
+namespace fd {
+
+namespace {
+
+constexpr int kTableThreads = 1024;  // the one CTA of a table kernel
+
+// ---- block-wide helpers of the table kernels (kTableThreads threads) -----------------------------
+
+// Inclusive sum over the block's threads; *total (all threads) the sum. s_warp: 32 entries.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const T u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();  // s_warp is free again
+  if (lane == 31) s_warp[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    T w = s_warp[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const T u = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += u;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  *total = s_warp[31];
+  return warp > 0 ? v + s_warp[warp - 1] : v;
+}
+
+// Leading non-negative entries among row[0, limit), by one warp (the same value in every lane).
+__device__ __forceinline__ int leading_pages(const int32_t* row, int limit) {
+  const int lane = threadIdx.x & 31;
+  for (int c0 = 0; c0 < limit; c0 += 128) {
+    int32_t e[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int c = c0 + 32 * k + lane;
+      e[k] = c < limit ? row[c] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const unsigned neg = __ballot_sync(0xffffffffu, e[k] < 0);
+      if (neg) return min(limit, c0 + 32 * k + __ffs(neg) - 1);
+    }
+  }
+  return limit;
+}
+
+// Visit free pages (page_refs == 0) lowest index first: give(rank, page) for rank = 0 .. need - 1.
+// Returns how many there were (need, or all of them when there are fewer). Four 16-byte loads a
+// thread are in flight, i.e. 16384 pages a round; the four counts (each sum at most 4096) are
+// scanned together as 16-bit fields.
+template <typename Give>
+__device__ __forceinline__ int64_t visit_free_pages(const int32_t* refs, int num_pages, int64_t need,
+                                                    unsigned long long* s_warp, Give give) {
+  const bool vec = (reinterpret_cast<uintptr_t>(refs) & 15u) == 0;
+  int64_t base = 0;
+  for (int64_t p0 = 0; p0 < num_pages && base < need; p0 += 16 * kTableThreads) {
+    int32_t r[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t p = p0 + 4 * (static_cast<int64_t>(k) * kTableThreads + threadIdx.x);
+      if (vec && p + 4 <= num_pages) {
+        const int4 v = *reinterpret_cast<const int4*>(refs + p);
+        r[k][0] = v.x; r[k][1] = v.y; r[k][2] = v.z; r[k][3] = v.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[k][i] = p + i < num_pages ? refs[p + i] : 1;
+      }
+    }
+    unsigned long long cnt = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        cnt += static_cast<unsigned long long>(r[k][i] == 0) << (16 * k);
+    unsigned long long all;
+    const unsigned long long before = block_scan(cnt, s_warp, &all) - cnt;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      int64_t rank = base + static_cast<int64_t>((before >> (16 * k)) & 0xffffu);
+      const int64_t p = p0 + 4 * (static_cast<int64_t>(k) * kTableThreads + threadIdx.x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (r[k][i] == 0) {
+          if (rank < need) give(rank, static_cast<int32_t>(p + i));
+          ++rank;
+        }
+      base += static_cast<int64_t>((all >> (16 * k)) & 0xffffu);
+    }
+  }
+  return base < need ? base : need;
+}
+
+// Index of the first entry of the increasing array s[0, n) that is > x (n when there is none).
+template <typename T>
+__device__ __forceinline__ int upper_bound(const T* s, int n, T x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (s[mid] > x) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Inclusive sums of the values s[0, n) in place, by the block (n <= kMaxPlanBatch).
+__device__ __forceinline__ int64_t scan_array(int64_t* s, int n, int64_t* s_warp) {
+  int64_t run = 0;
+  for (int i0 = 0; i0 < n; i0 += kTableThreads) {
+    const int i = i0 + threadIdx.x;
+    int64_t total;
+    const int64_t v = block_scan<int64_t>(i < n ? s[i] : 0, s_warp, &total);
+    if (i < n) s[i] = run + v;
+    run += total;
+  }
+  __syncthreads();
+  return run;
+}
+
+// ---- append ---------------------------------------------------------------------------------------
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendRows = 32;  // rows whose places one CTA looks up together
+
+// 16 destination bytes from the source elements at src.
+template <typename S, bool kFp8>
+__device__ __forceinline__ uint4 append_unit(const S* src, float scale) {
+  if constexpr (!kFp8) {
+    return __ldg(reinterpret_cast<const uint4*>(src));
+  } else {
+    float x[16];
+    if constexpr (sizeof(S) == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(src) + i);
+        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // a bf16 is the upper half of the fp32 of the same value
+          x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+          x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+      }
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t lo, hi;
+      const float a = __fdiv_rn(x[4 * i], scale), b = __fdiv_rn(x[4 * i + 1], scale);
+      const float c = __fdiv_rn(x[4 * i + 2], scale), d = __fdiv_rn(x[4 * i + 3], scale);
+      asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(lo) : "f"(a), "f"(b));
+      asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(hi) : "f"(c), "f"(d));
+      o[i] = lo | (hi << 16);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
+
+// A CTA takes p.rows_per_cta packed rows. Every thread sums new_lens (the ends of the sequences,
+// shared memory); one thread a row finds the row's sequence, page and slot; then all threads copy
+// the rows' K and V in 16-byte units of the destination.
+template <typename S, bool kFp8>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+  extern __shared__ int64_t s_end[];  // [batch] ends of the sequences' packed rows
+  __shared__ int64_t s_warp[kAppendThreads / 32];
+  __shared__ int64_t s_k[kAppendRows], s_v[kAppendRows];  // element offset of the row's place, < 0: none
+  __shared__ int64_t s_total;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t run = 0;
+  for (int i0 = 0; i0 < p.batch; i0 += kAppendThreads) {
+    const int i = i0 + tid;
+    int64_t v = i < p.batch ? max(0, p.new_lens[i]) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    int64_t before = run;
+    for (int w = 0; w < kAppendThreads / 32; ++w) {
+      if (w < warp) before += s_warp[w];
+      run += s_warp[w];
+    }
+    if (i < p.batch) s_end[i] = before + v;
+  }
+  if (tid == 0) s_total = run;
+  __syncthreads();
+  const int64_t total = s_total;
+  if (total > p.rows) {
+    if (tid == 0 && blockIdx.x == 0) atomicOr(p.status, FD_FLAG_LEN_CLAMPED);
+    return;
+  }
+  const int64_t cap = static_cast<int64_t>(p.pages_per_seq) * p.page_size;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_cta; r0 < total;
+       r0 += static_cast<int64_t>(gridDim.x) * p.rows_per_cta) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(p.rows_per_cta), total - r0));
+    if (tid < n) {
+      const int64_t r = r0 + tid;
+      const int b = upper_bound(s_end, p.batch, r);
+      const int64_t start = b > 0 ? s_end[b - 1] : 0;
+      const int64_t pos = static_cast<int64_t>(p.start_lens[b]) + (r - start);
+      int64_t place = -1, place_v = -1;
+      if (p.start_lens[b] < 0 || pos >= cap) {
+        atomicOr(p.status, FD_FLAG_LEN_CLAMPED);
+      } else {
+        const int page = p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + pos / p.page_size];
+        if (page < 0 || page >= p.num_pages) {
+          atomicOr(p.status, FD_FLAG_BAD_PAGE);
+        } else {
+          place = page * p.pool_sp + (pos % p.page_size) * p.d;
+          place_v = place;
+        }
+      }
+      s_k[tid] = place;
+      s_v[tid] = place_v;
+    }
+    __syncthreads();
+    const int per_head = p.d * (kFp8 ? 1 : static_cast<int>(sizeof(S))) / 16;  // a power of two
+    const int shift = __ffs(per_head) - 1;
+    const int elems = p.d / per_head;  // elements of one unit
+    const int half = p.hkv * per_head;
+    for (int i = 0; i < n; ++i) {
+      if (s_k[i] < 0) continue;
+      for (int u = tid; u < 2 * half; u += kAppendThreads) {
+        const bool is_v = u >= half;
+        const int w = is_v ? u - half : u;
+        const int h = w >> shift, e = (w & (per_head - 1)) * elems;
+        const S* src = is_v ? static_cast<const S*>(p.v_new) + (r0 + i) * p.v_sr + h * p.v_sh + e
+                            : static_cast<const S*>(p.k_new) + (r0 + i) * p.k_sr + h * p.k_sh + e;
+        const uint4 x = append_unit<S, kFp8>(src, is_v ? p.v_scale : p.k_scale);
+        const int64_t at = (is_v ? s_v[i] : s_k[i]) + h * p.pool_sh + e;
+        char* dst = static_cast<char*>(is_v ? p.v_pages : p.k_pages) + at * (kFp8 ? 1 : static_cast<int>(sizeof(S)));
+        *reinterpret_cast<uint4*>(dst) = x;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---- reserve --------------------------------------------------------------------------------------
+
+// One CTA. A warp a sequence counts its pages; the missing ones, summed over the sequences, are the
+// ranks of the free pages that visit_free_pages gives. If they run out, the sequences whose sum
+// exceeds what there was give back what they got.
+__global__ void __launch_bounds__(kTableThreads) reserve_kernel(const ReserveParams p) {
+  extern __shared__ int64_t s_sum[];  // [batch] inclusive sums of the missing pages
+  int32_t* s_have = reinterpret_cast<int32_t*>(s_sum + p.batch);
+  __shared__ int64_t s_warp[32];
+  __shared__ unsigned long long s_warp2[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int b = warp; b < p.batch; b += kTableThreads / 32) {
+    int64_t want = (max(static_cast<int64_t>(p.want_lens[b]), int64_t(0)) + p.page_size - 1) / p.page_size;
+    if (want > p.pages_per_seq) {
+      want = p.pages_per_seq;
+      if (lane == 0) atomicOr(p.status, FD_FLAG_LEN_CLAMPED);
+    }
+    const int have = leading_pages(p.block_table + static_cast<int64_t>(b) * p.pages_per_seq, static_cast<int>(want));
+    if (lane == 0) {
+      s_have[b] = have;
+      s_sum[b] = want - have;
+    }
+  }
+  __syncthreads();
+  const int64_t need = scan_array(s_sum, p.batch, s_warp);
+  if (need == 0) return;
+  auto entry = [&](int64_t rank) {
+    const int b = upper_bound(s_sum, p.batch, rank);
+    return p.block_table + static_cast<int64_t>(b) * p.pages_per_seq + s_have[b] + (rank - (b > 0 ? s_sum[b - 1] : 0));
+  };
+  const int64_t got = visit_free_pages(p.page_refs, p.num_pages, need, s_warp2, [&](int64_t rank, int32_t page) {
+    *entry(rank) = page;
+    p.page_refs[page] = 1;
+  });
+  if (got < need) {
+    if (threadIdx.x == 0) atomicOr(p.status, FD_FLAG_POOL_FULL);
+    __syncthreads();
+    const int b = upper_bound(s_sum, p.batch, got);  // the first sequence that is not served
+    for (int64_t r = (b > 0 ? s_sum[b - 1] : 0) + threadIdx.x; r < got; r += kTableThreads) {
+      int32_t* e = entry(r);
+      p.page_refs[*e] = 0;
+      *e = -1;
+    }
+  }
+}
+
+// ---- fork -----------------------------------------------------------------------------------------
+
+// One CTA plans the pairs: checks, new pages, rows and references; the copies of the last pages'
+// rows (p.copies) are fork_copy_kernel's.
+__global__ void __launch_bounds__(kTableThreads) fork_plan_kernel(const ForkParams p) {
+  extern __shared__ int64_t s_sum[];  // [count] inclusive sums of the new pages
+  int32_t* s_len = reinterpret_cast<int32_t*>(s_sum + p.count);  // [count] tokens, -1: skipped
+  int32_t* s_page = s_len + p.count;                             // [count] new page
+  int32_t* s_owner = s_page + p.count;                           // [batch] first pair of a destination
+  __shared__ int64_t s_warp[32];
+  __shared__ unsigned long long s_warp2[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int b = threadIdx.x; b < p.batch; b += kTableThreads) s_owner[b] = INT32_MAX;
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.count; i += kTableThreads) {
+    const int dst = p.dst_seqs[i];
+    if (dst >= 0 && dst < p.batch) atomicMin(&s_owner[dst], i);
+  }
+  __syncthreads();
+  for (int i = warp; i < p.count; i += kTableThreads / 32) {
+    const int src = p.src_seqs[i], dst = p.dst_seqs[i];
+    int len = -1;
+    uint32_t flag = 0;
+    if (src < 0 || src >= p.batch || dst < 0 || dst >= p.batch || s_owner[dst] != i ||
+        p.block_table[static_cast<int64_t>(dst) * p.pages_per_seq] >= 0) {
+      flag = FD_FLAG_BAD_INDEX;
+    } else {
+      len = p.cache_lens[src];
+      const int64_t pages = (static_cast<int64_t>(len) + p.page_size - 1) / p.page_size;
+      bool ok = len >= 0 && pages <= p.pages_per_seq;
+      const int32_t* row = p.block_table + static_cast<int64_t>(src) * p.pages_per_seq;
+      for (int64_t c = lane; ok && c < pages; c += 32)
+        ok = row[c] >= 0 && row[c] < p.num_pages && p.page_refs[row[c]] > 0;
+      if (!__all_sync(0xffffffffu, ok)) {
+        len = -1;
+        flag = FD_FLAG_BAD_PAGE;
+      }
+    }
+    if (lane == 0) {
+      if (flag) atomicOr(p.status, flag);
+      s_len[i] = len;
+      s_sum[i] = len > 0 && len % p.page_size != 0 ? 1 : 0;
+    }
+  }
+  __syncthreads();
+  const int64_t need = scan_array(s_sum, p.count, s_warp);
+  const int64_t got = visit_free_pages(p.page_refs, p.num_pages, need, s_warp2, [&](int64_t rank, int32_t page) {
+    s_page[upper_bound(s_sum, p.count, rank)] = page;
+  });
+  if (got < need && threadIdx.x == 0) atomicOr(p.status, FD_FLAG_POOL_FULL);
+  __syncthreads();
+  for (int i = warp; i < p.count; i += kTableThreads / 32) {
+    const int len = s_len[i];
+    const bool fresh = s_sum[i] > (i > 0 ? s_sum[i - 1] : 0);
+    int4 copy = make_int4(0, 0, 0, 0);
+    if (len >= 0 && (!fresh || s_sum[i] <= got)) {
+      const int src = p.src_seqs[i], dst = p.dst_seqs[i];
+      const int full = len / p.page_size;
+      const int32_t* from = p.block_table + static_cast<int64_t>(src) * p.pages_per_seq;
+      int32_t* to = p.block_table + static_cast<int64_t>(dst) * p.pages_per_seq;
+      for (int c = lane; c < p.pages_per_seq; c += 32) {
+        int32_t page = -1;
+        if (c < full) {
+          page = from[c];
+          atomicAdd(&p.page_refs[page], 1);
+        } else if (c == full && fresh) {
+          page = s_page[i];
+          atomicAdd(&p.page_refs[page], 1);
+        }
+        to[c] = page;
+      }
+      if (lane == 0) {
+        p.cache_lens[dst] = len;
+        if (fresh) copy = make_int4(from[full], s_page[i], len % p.page_size, 0);
+      }
+    }
+    if (lane == 0) p.copies[i] = copy;
+  }
+}
+
+constexpr int kCopyThreads = 256;
+
+// Block (i, j): the K (j even) or V rows of KV head j / 2 of copy i, contiguous in both pages.
+__global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const ForkParams p) {
+  const int4 c = p.copies[blockIdx.x];
+  if (c.z == 0) return;
+  const int h = blockIdx.y >> 1;
+  char* pool = static_cast<char*>((blockIdx.y & 1) ? p.v_pages : p.k_pages);
+  const uint4* src = reinterpret_cast<const uint4*>(pool + c.x * p.pool_sp + h * p.pool_sh);
+  uint4* dst = reinterpret_cast<uint4*>(pool + c.y * p.pool_sp + h * p.pool_sh);
+  const int64_t n = static_cast<int64_t>(c.z) * p.row_bytes / 16;
+  for (int64_t u = threadIdx.x; u < n; u += kCopyThreads) dst[u] = src[u];
+}
+
+// ---- free -----------------------------------------------------------------------------------------
+
+constexpr int kFreeThreads = 128;
+
+// One CTA a listed sequence; the first of equal entries frees it.
+__global__ void __launch_bounds__(kFreeThreads) free_kernel(const FreeParams p) {
+  const int i = blockIdx.x, tid = threadIdx.x;
+  const int b = p.seqs[i];
+  if (b < 0 || b >= p.batch) {
+    if (tid == 0) atomicOr(p.status, FD_FLAG_BAD_INDEX);
+    return;
+  }
+  bool first = true;
+  for (int j = tid; j < i; j += kFreeThreads) first = first && p.seqs[j] != b;
+  if (!__syncthreads_and(first)) return;
+  int32_t* row = p.block_table + static_cast<int64_t>(b) * p.pages_per_seq;
+  for (int c0 = 0; c0 < p.pages_per_seq; c0 += kFreeThreads) {
+    const int c = c0 + tid;
+    const int32_t page = c < p.pages_per_seq ? row[c] : -1;
+    // the sequence's pages end at the first negative entry, wherever it stands in this stretch
+    __shared__ int s_end;
+    __syncthreads();
+    if (tid == 0) s_end = kFreeThreads;
+    __syncthreads();
+    if (page < 0) atomicMin(&s_end, tid);
+    __syncthreads();
+    if (tid < s_end) {
+      row[c] = -1;
+      drop_reference(p.page_refs, p.num_pages, page, p.status);
+    }
+    if (s_end < kFreeThreads) break;
+  }
+  if (tid == 0) p.cache_lens[b] = 0;
+}
+
+// ---- compact --------------------------------------------------------------------------------------
+
+constexpr int kCompactThreads = 256;
+
+// Whether sequence b's compaction is valid (all threads get the answer); *first: its first moved
+// index. Reads the table and the references, which no CTA of compact_move_kernel writes.
+__device__ __forceinline__ bool check_compact(const CompactParams& p, int b, int m, int* first, bool report) {
+  const int32_t start = p.start_lens[b];
+  const int32_t* keep = p.keep + static_cast<int64_t>(b) * p.max_keep;
+  const int64_t cap = static_cast<int64_t>(p.pages_per_seq) * p.page_size;
+  __shared__ int s_first;
+  __syncthreads();
+  if (threadIdx.x == 0) s_first = m;
+  __syncthreads();
+  bool ok = start >= 0 && m <= p.max_keep;
+  if (ok) {
+    for (int i = threadIdx.x; i < m; i += kCompactThreads) {
+      const int k = keep[i];
+      ok = ok && k > (i > 0 ? keep[i - 1] : -1);
+      if (k != i) atomicMin(&s_first, i);
+    }
+  }
+  const int64_t last = m > 0 && ok ? static_cast<int64_t>(start) + keep[m - 1] : static_cast<int64_t>(start) + m - 1;
+  ok = ok && last < cap && static_cast<int64_t>(start) + m <= cap;
+  if (!__syncthreads_and(ok)) {
+    if (report && threadIdx.x == 0) atomicOr(p.status, FD_FLAG_BAD_INDEX);
+    return false;
+  }
+  *first = s_first;
+  if (s_first >= m) return true;
+  // the pages from the first moved position to the last one read; the written ones are unshared
+  const int64_t c0 = (static_cast<int64_t>(start) + s_first) / p.page_size, c1 = last / p.page_size;
+  const int64_t cw = (static_cast<int64_t>(start) + m - 1) / p.page_size;
+  const int32_t* row = p.block_table + static_cast<int64_t>(b) * p.pages_per_seq;
+  for (int64_t c = threadIdx.x; c <= c1; c += kCompactThreads) {
+    const int32_t page = row[c];
+    ok = ok && page >= 0 && (c < c0 || (page < p.num_pages && (c > cw || p.page_refs[page] == 1)));
+  }
+  if (!__syncthreads_and(ok)) {
+    if (report && threadIdx.x == 0) atomicOr(p.status, FD_FLAG_BAD_PAGE);
+    return false;
+  }
+  return true;
+}
+
+// Block (b, j): moves the rows of K (j even) or V, KV head j / 2, of sequence b. The list increases
+// strictly, so a row read lies at or behind the row written for it and behind every row written for
+// an earlier one: kMove rows a thread are read, then (after a barrier) written, front to back.
+constexpr int kMove = 4;
+__global__ void __launch_bounds__(kCompactThreads) compact_move_kernel(const CompactParams p) {
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int m = p.keep_lens[b];
+  int first = 0;
+  const bool go = m >= 0 && check_compact(p, b, m, &first, blockIdx.y == 0);
+  if (blockIdx.y == 0 && tid == 0) p.valid[b] = go ? 1 : 0;
+  if (!go) return;
+  const int h = blockIdx.y >> 1;
+  char* pool = static_cast<char*>((blockIdx.y & 1) ? p.v_pages : p.k_pages) + h * p.pool_sh;
+  const int units = p.row_bytes / 16;  // 4 .. 32, a power of two
+  const int per = kCompactThreads / units;
+  const int unit = tid & (units - 1), slot = tid / units;
+  const int32_t start = p.start_lens[b];
+  const int32_t* keep = p.keep + static_cast<int64_t>(b) * p.max_keep;
+  const int32_t* row = p.block_table + static_cast<int64_t>(b) * p.pages_per_seq;
+  auto at = [&](int pos) {
+    return reinterpret_cast<uint4*>(pool + row[pos / p.page_size] * p.pool_sp +
+                                    static_cast<int64_t>(pos % p.page_size) * p.row_bytes) + unit;
+  };
+  for (int i0 = first; i0 < m; i0 += kMove * per) {
+    uint4 x[kMove];
+#pragma unroll
+    for (int k = 0; k < kMove; ++k) {
+      const int i = i0 + k * per + slot;
+      if (i < m) x[k] = *at(start + keep[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kMove; ++k) {
+      const int i = i0 + k * per + slot;
+      if (i < m) *at(start + i) = x[k];
+    }
+    __syncthreads();
+  }
+}
+
+// One CTA a sequence: the new length, the pages behind it given back.
+__global__ void __launch_bounds__(kFreeThreads) compact_table_kernel(const CompactParams p) {
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int m = p.keep_lens[b];
+  if (m < 0 || !p.valid[b]) return;
+  const int64_t len = static_cast<int64_t>(p.start_lens[b]) + m;
+  int32_t* row = p.block_table + static_cast<int64_t>(b) * p.pages_per_seq;
+  const int from = static_cast<int>((len + p.page_size - 1) / p.page_size);
+  __shared__ int s_end;
+  if (tid < 32) {
+    const int n = leading_pages(row, p.pages_per_seq);
+    if (tid == 0) s_end = n;
+  }
+  __syncthreads();
+  for (int c = from + tid; c < s_end; c += kFreeThreads) {
+    const int32_t page = row[c];
+    row[c] = -1;
+    drop_reference(p.page_refs, p.num_pages, page, p.status);
+  }
+  if (tid == 0) p.cache_lens[b] = static_cast<int32_t>(len);
+}
+
+}  // namespace
+
+// ---- launchers ------------------------------------------------------------------------------------
+
+template <typename S, bool kFp8>
+static cudaError_t launch_append_t(const AppendParams& p, int grid, cudaStream_t stream) {
+  append_kernel<S, kFp8><<<grid, kAppendThreads, sizeof(int64_t) * p.batch, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_append(AppendParams p, int src_dtype, bool fp8, int nsm, cudaStream_t stream) {
+  const int64_t want = (p.rows + 8 * nsm - 1) / (8 * nsm);
+  p.rows_per_cta = static_cast<int>(want < 1 ? 1 : want > kAppendRows ? kAppendRows : want);
+  int64_t grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
+  if (grid > 16 * nsm) grid = 16 * nsm;
+  const int g = static_cast<int>(grid);
+  if (src_dtype == FD_F32) return fp8 ? launch_append_t<float, true>(p, g, stream) : launch_append_t<float, false>(p, g, stream);
+  return fp8 ? launch_append_t<__nv_bfloat16, true>(p, g, stream) : launch_append_t<__nv_bfloat16, false>(p, g, stream);
+}
+
+static cudaError_t allow_smem(const void* f, size_t bytes) {
+  return bytes <= 48 * 1024 ? cudaSuccess
+                            : cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+}
+
+cudaError_t launch_reserve(const ReserveParams& p, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(p.batch) * 12;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(reserve_kernel), smem);
+  if (e != cudaSuccess) return e;
+  reserve_kernel<<<1, kTableThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(p.count) * 16 + static_cast<size_t>(p.batch) * 4;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fork_plan_kernel), smem);
+  if (e != cudaSuccess) return e;
+  fork_plan_kernel<<<1, kTableThreads, smem, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  fork_copy_kernel<<<dim3(p.count, 2 * p.hkv), kCopyThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_free(const FreeParams& p, cudaStream_t stream) {
+  free_kernel<<<p.count, kFreeThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
+  compact_move_kernel<<<dim3(p.batch, 2 * p.hkv), kCompactThreads, 0, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  compact_table_kernel<<<p.batch, kFreeThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace fd
