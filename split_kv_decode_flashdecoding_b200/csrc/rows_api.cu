@@ -4,6 +4,7 @@
 
 #include "abi_internal.h"
 #include "rows.h"
+#include "rows_plan.h"
 
 using namespace fd;
 using namespace fd_abi;
@@ -51,16 +52,34 @@ fd_status resolve_rows(const fd_tensor* q, const fd_tensor* out, int64_t hkv, in
   p->hkv = static_cast<int32_t>(hkv);
   p->g = static_cast<int32_t>(hq / hkv);
   p->d = static_cast<int32_t>(d);
+  p->g_recip16 = (65536 + p->g - 1) / p->g;
   p->scale_log2 = static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)) * 1.4426950408889634);
   return FD_OK;
 }
 
-fd_status run_rows(RowsParams* p, cudaStream_t stream) {
+int row_ctas(int nsm) { return std::min(nsm, kMaxRowCtas); }
+
+// Launch on all multiprocessors. kd / ks: dimensions and byte strides of the K map (ksv: of the V map).
+fd_status run_rows(RowsParams* p, int kv_rank, const uint64_t* kd, const uint64_t* ks, const uint64_t* vs,
+                   const uint32_t* kb, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const int nctas = row_ctas(sm_count(dev));
+  if (nctas < 1) return fail(FD_ERR_CUDA, "no multiprocessors reported for device %d", dev);
   void* ws = nullptr;
-  fd_status s = get_workspace(stream, sizeof(WsHeader), &ws, nullptr);
+  fd_status s = get_workspace(stream, rows_workspace_bytes(p->d, nctas), &ws, nullptr);
   if (s != FD_OK) return s;
   p->hdr = static_cast<WsHeader*>(ws);
-  const cudaError_t e = launch_rows(*p, stream);
+  CUtensorMap tq, tk, tv;
+  p->q_box_rows = std::min(rows_tile_tokens(p->g), p->rows);
+  const uint64_t qd[3] = {static_cast<uint64_t>(p->d), static_cast<uint64_t>(p->hq), static_cast<uint64_t>(p->rows)};
+  const uint64_t qs[2] = {static_cast<uint64_t>(p->q_sh) * 2, static_cast<uint64_t>(p->q_sr) * 2};
+  const uint32_t qb[3] = {64, static_cast<uint32_t>(p->g), static_cast<uint32_t>(p->q_box_rows)};
+  if ((s = make_tmap(&tq, p->q, 3, qd, qs, qb, "q")) != FD_OK) return s;
+  if ((s = make_tmap(&tk, p->k, kv_rank, kd, ks, kb, "k")) != FD_OK) return s;
+  if ((s = make_tmap(&tv, p->v, kv_rank, kd, vs, kb, "v")) != FD_OK) return s;
+  e = launch_rows(*p, tq, tk, tv, nctas, stream);
   return e == cudaSuccess ? FD_OK : cuda_fail(e, "attention kernel launch");
 }
 
@@ -117,7 +136,13 @@ fd_status tree(const fd_tensor* q, const fd_tensor* k, const fd_tensor* v, const
   p.prefix_lens = prefix_lens;
   p.mask = reinterpret_cast<const uint32_t*>(tree_mask);
   p.mask_words = mask_words;
-  return run_rows(&p, stream);
+  p.kv_box_rows = std::min(128, paged ? p.page_size : p.cap);
+  const uint64_t kd[4] = {static_cast<uint64_t>(p.d), static_cast<uint64_t>(k->shape[2]), static_cast<uint64_t>(p.hkv),
+                          static_cast<uint64_t>(k->shape[0])};
+  const uint64_t ks[3] = {static_cast<uint64_t>(k->stride[2]) * 2, static_cast<uint64_t>(k->stride[1]) * 2,
+                          static_cast<uint64_t>(k->stride[0]) * 2};
+  const uint32_t kb[4] = {64, static_cast<uint32_t>(p.kv_box_rows), 1, 1};
+  return run_rows(&p, 4, kd, ks, ks, kb, stream);
 }
 
 }  // namespace
@@ -146,7 +171,12 @@ fd_status fd_prompt_attention(const fd_tensor* q, const fd_tensor* k, const fd_t
   p.lse = lse;
   p.row_lens = seq_lens;
   p.cap = p.rows;
-  return run_rows(&p, static_cast<cudaStream_t>(stream));
+  p.kv_box_rows = std::min(128, p.rows);
+  const uint64_t kd[3] = {static_cast<uint64_t>(p.d), static_cast<uint64_t>(p.hkv), static_cast<uint64_t>(p.rows)};
+  const uint64_t ks[2] = {static_cast<uint64_t>(p.k_sh) * 2, static_cast<uint64_t>(p.k_sr) * 2};
+  const uint64_t vs[2] = {static_cast<uint64_t>(p.v_sh) * 2, static_cast<uint64_t>(p.v_sr) * 2};
+  const uint32_t kb[3] = {64, 1, static_cast<uint32_t>(p.kv_box_rows)};
+  return run_rows(&p, 3, kd, ks, vs, kb, static_cast<cudaStream_t>(stream));
 }
 
 fd_status fd_tree_attention(const fd_tensor* q, const fd_tensor* k_cache, const fd_tensor* v_cache,
@@ -170,13 +200,13 @@ fd_status fd_tree_attention_paged(const fd_tensor* q, const fd_tensor* k_pages,
 size_t fd_prompt_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_q_heads,
                                  int32_t num_kv_heads, int32_t head_dim) {
   if (batch < 0 || total_rows < 0 || num_q_heads < 1 || num_kv_heads < 1 || head_dim < 1) return 0;
-  return sizeof(WsHeader);
+  return rows_workspace_bytes(head_dim, kMaxRowCtas);
 }
 
 size_t fd_tree_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_q_heads,
                                int32_t num_kv_heads, int32_t cache_capacity, int32_t head_dim) {
   if (batch < 0 || total_rows < 0 || num_q_heads < 1 || num_kv_heads < 1 || cache_capacity < 0 || head_dim < 1) return 0;
-  return sizeof(WsHeader);
+  return rows_workspace_bytes(head_dim, kMaxRowCtas);
 }
 
 }  // extern "C"

@@ -1,0 +1,85 @@
+// How the attention of packed query rows (rows_tc.cu) is divided over the CTAs.
+//
+// Request b with n rows is cut into items of 2 T tokens, T = 128 / G: an item is up to two 128-row
+// tiles (T tokens of all G query heads of one KV head) that walk the same key tiles. The items of
+// all (request, KV head, token pair) stand in one line, each as long as its work, counted in 1/128
+// of a key tile plus a fixed part; CTA i of n takes the stretch [W i / n, W (i + 1) / n). An item
+// that a stretch ends in is cut at the key tile in proportion, so that every CTA has the same work
+// whatever the lengths are; its pieces are merged by the last of their CTAs to finish. A cut that
+// would leave a piece below kMinPiece key tiles is moved to the item's nearer end: such a piece
+// costs less than a merge does. Every CTA derives its own stretch from the lengths; there is no plan
+// in memory.
+#pragma once
+
+#include <stdint.h>
+
+#include "plan.h"
+
+namespace fd {
+
+constexpr int32_t kItemFixed = 256;  // an item's fixed cost (Q, first scores, output): two key tiles
+constexpr int32_t kMinPiece = 4;     // key tiles of the smallest piece of a cut item
+constexpr int32_t kMaxRowCtas = 192; // CTAs of one call (merge counters in the workspace header)
+
+FD_HD int32_t rows_tile_tokens(int32_t g) { return kQTile / g; }
+FD_HD int32_t rows_pairs(int32_t n, int32_t tpt) { return cdiv32(n, 2 * tpt); }
+
+// Work of the first u items of one (request, KV head). A prompt's item u sees 2 T (u + 1) keys, taken
+// as half a tile more on average when rounded up to tiles; every item of a tree sees all its keys.
+FD_HD int64_t rows_weight(bool causal, int32_t tpt, int32_t keys, int64_t u) {
+  return causal ? u * (kItemFixed + 64) + tpt * u * (u + 1)
+                : u * (kItemFixed + static_cast<int64_t>(cdiv32(keys, 128)) * 128);
+}
+
+// Keys that item u of a request sees.
+FD_HD int32_t rows_item_keys(bool causal, int32_t tpt, int32_t n, int32_t keys, int32_t u) {
+  if (!causal) return keys;
+  const int64_t end = static_cast<int64_t>(u + 1) * 2 * tpt;
+  return end < n ? static_cast<int32_t>(end) : n;
+}
+
+// CTAs that take part: as many as there are items, or as there are stretches of kMinPiece tiles.
+FD_HD int32_t rows_active(int64_t weight, int64_t items, int32_t nctas) {
+  const int64_t n = weight / (kMinPiece * 128);
+  const int64_t m = items > n ? items : n;
+  return m < nctas ? (m < 1 ? 1 : static_cast<int32_t>(m)) : nctas;
+}
+
+// Where CTA i's stretch begins.
+FD_HD int64_t rows_bound(int64_t weight, int32_t nact, int32_t i) {
+  return weight / nact * i + weight % nact * i / nact;
+}
+
+// The key tile at which the point x of the line cuts an item of `tiles` key tiles at [a, a + w).
+FD_HD int32_t rows_cut(int64_t x, int64_t a, int64_t w, int32_t tiles) {
+  if (x <= a) return 0;
+  if (x >= a + w) return tiles;
+  const int32_t t = static_cast<int32_t>(tiles * (x - a) / w);
+  if (t < kMinPiece) return 0;
+  return tiles - t < kMinPiece ? tiles : t;
+}
+
+// The cuts of an item: bounds first .. first + count - 1 cut it (count 0: one CTA has all of it).
+// Bounds that lie inside the item without cutting it stand at its ends, a few at most.
+FD_HD void rows_cuts(int64_t weight, int32_t nact, int64_t a, int64_t w, int32_t tiles, int32_t cta,
+                     int32_t* first, int32_t* count) {
+  int32_t lo = cta, hi = cta;  // a bound in or at the item: the caller's own stretch meets the item
+  while (lo > 0 && rows_cut(rows_bound(weight, nact, lo), a, w, tiles) > 0) {
+    // step down in strides as long as the bound stays inside
+    int32_t step = 1;
+    while (lo - 2 * step > 0 && rows_cut(rows_bound(weight, nact, lo - 2 * step), a, w, tiles) > 0) step *= 2;
+    lo -= step;
+  }
+  ++lo;
+  while (rows_cut(rows_bound(weight, nact, lo), a, w, tiles) == 0) ++lo;  // bounds snapped to the start
+  if (hi < lo) hi = lo;
+  while (hi < nact && rows_cut(rows_bound(weight, nact, hi), a, w, tiles) < tiles) {
+    int32_t step = 1;
+    while (hi + 2 * step < nact && rows_cut(rows_bound(weight, nact, hi + 2 * step), a, w, tiles) < tiles) step *= 2;
+    hi += step;
+  }
+  *first = lo;
+  *count = hi - lo;
+}
+
+}  // namespace fd

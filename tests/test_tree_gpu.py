@@ -216,5 +216,7 @@ def test_same_results_again_and_in_a_graph():
     out.fill_(9.0)
     g.replay()
     torch.cuda.synchronize()
-    assert torch.equal(out[:16], first[0][:16]) and bool((out[18:] == 9.0).all())
+    assert bool((out[18:] == 9.0).all())
+    # other lengths may cut the first request's keys elsewhere: the bounds hold, not every bit
+    ref.check_rows(out[:16], lse[:16], ref.tree(c.q[:16], c.caches[:1], c.prefix[:1], [16], c.see[:1]))
     assert fd.fd_poll_status(stream=s) == 0
