@@ -27,7 +27,9 @@
 // which one that is.
 //
 // Warps: 0-3 and 4-7 softmax of lanes 0 and 1 (warp w reads TMEM lanes 32 (w mod 4) + [0, 32), one row a
-// thread); 8-11 epilogue; 12 plan and TMA; 13, 14 tensor-core issue of lanes 0 and 1.
+// thread); 8-11 epilogue; 12 plan and TMA; 13 tensor-core issue.
+#include <type_traits>
+
 #include "common.cuh"
 #include "rows.h"
 #include "rows_plan.h"
@@ -43,6 +45,8 @@ constexpr uint32_t kRwTmemCols = 512;
 constexpr uint32_t kRwColO = 256;              // O of lane L at kRwColO + L D; S / P of lane L at 128 L
 constexpr uint32_t kRwHalf = 128 * 64 * 2;     // bytes of one 64-column half of a 128-row tile
 constexpr float kRwRescale = 8.0f;             // log2 units
+constexpr int kRwPolyEvery = 4;                // of a row's pairs of exponentials, one on the FMA pipe
+constexpr uint32_t kRwWaitClocks = 0x80000000u;
 
 enum RowSource { kSrcPacked = 0, kSrcCache = 1, kSrcPaged = 2 };
 
@@ -55,6 +59,9 @@ struct RowItem {
   int32_t k1;               // keys of the item (all pieces): tiles hold keys < k1
   int32_t prefix;           // tree: keys every row sees
   int32_t alt;              // one row tile, the lanes take alternate key tiles
+  // by lane: its tokens, the key tiles it uses, the end of its visible keys from tile0's first key on.
+  // The i-th tile of lane L is tile0 + i, or tile0 + 2 i + L (alt).
+  int32_t tokens[2], used[2], kend[2];
   int32_t cut0, cuts, piece;  // rows_cuts of a cut item (cuts 0: whole), this piece's index
 };
 
@@ -66,13 +73,18 @@ struct __align__(1024) RwSmem {
   __nv_bfloat16 kv[kStages][kHalves][128 * 64];
   RowItem item[kRwItems];
   float mfin[2][2][128], lfin[2][2][128];  // [item parity][lane][row]
-  int64_t part_w[kRwThreads];              // plan: work, rows and items of a thread's requests
-  int32_t part_r[kRwThreads], part_i[kRwThreads];
+  union {
+    struct {  // plan: work, rows and items of a thread's requests
+      int64_t part_w[kRwThreads];
+      int32_t part_r[kRwThreads], part_i[kRwThreads];
+    };
+    unsigned char stage[4][32][144];  // epilogue: 64 columns of a warp's rows, 16 bytes of padding each
+  };
   uint64_t full[kStages], empty[kStages];
   uint64_t qfull[2], qempty[2], ifull[kRwItems], iempty[kRwItems];
-  uint64_t sfull[2], pfull[2], pvdone[2], ofin[2], oempty[2];
+  uint64_t sfull[2], pfull[2][2], ofin[2], oempty[2];  // pfull: keys [0, 64) and [64, 128)
   uint64_t lready[2][2], lfree[2][2];
-  uint64_t drain[2];
+  uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
   int bad;
@@ -100,9 +112,35 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// 2^x for a pair, x <= 2^7, on the FMA pipe: the special-function unit gives 16 exponentials a clock,
+// which is as long for a tile as its two products, so every kRwPolyEvery-th pair is computed here.
+// x = n + f with n the nearest integer (in the low bits of x + 1.5 2^23) and 2^f, |f| <= 1/2, by the
+// polynomial of degree 5 with the least relative error (Remez exchange; 7.5e-8, 2.1e-7 evaluated in
+// fp32: below the 2^-22 of the hardware's). x below -126 counts as -126.
+__device__ __forceinline__ void exp2_poly(uint64_t x, float& lo, float& hi) {
+  const uint64_t magic = pair_f32(12582912.f, 12582912.f), back = pair_f32(-12582912.f, -12582912.f);
+  float x0, x1;
+  unpair_f32(x, x0, x1);
+  x = pair_f32(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const uint64_t t = add_f32x2(x, magic);
+  const uint64_t n = add_f32x2(t, back);
+  const uint64_t f = fma_f32x2(n, pair_f32(-1.f, -1.f), x);
+  uint64_t y = pair_f32(1.3276472454890609e-3f, 1.3276472454890609e-3f);
+  y = fma_f32x2(y, f, pair_f32(9.675540961325169e-3f, 9.675540961325169e-3f));
+  y = fma_f32x2(y, f, pair_f32(5.550713092088699e-2f, 5.550713092088699e-2f));
+  y = fma_f32x2(y, f, pair_f32(2.4022120237350464e-1f, 2.4022120237350464e-1f));
+  y = fma_f32x2(y, f, pair_f32(6.931469440460205e-1f, 6.931469440460205e-1f));
+  y = fma_f32x2(y, f, pair_f32(1.0000001192092896f, 1.0000001192092896f));
+  float t0, t1, y0, y1;
+  unpair_f32(t, t0, t1);
+  unpair_f32(y, y0, y1);
+  lo = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23));
+  hi = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23));
+}
+// Maximum that a NaN wins, so that a row which sees one becomes NaN as a whole.
 __device__ __forceinline__ float max3_f32(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -120,17 +158,16 @@ __device__ __forceinline__ void set_regs_less() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// The bounded waits of common.cuh with the polling loop in line: a kernel that re-divides its
-// registers between warps (setmaxnreg) cannot call a function. The status word is raised once, at
-// the kernel's end.
+// The bounded waits of common.cuh with a short polling loop in line: a kernel that re-divides its
+// registers between warps (setmaxnreg) cannot call a function. The limit counts clocks (2^31 are
+// 1.1 s at 1965 MHz); the status word is raised once, at the kernel's end.
 __device__ __forceinline__ bool row_poll(uint64_t* bar, uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  do {
+  const uint32_t t0 = static_cast<uint32_t>(clock());
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-  } while (global_timer_ns() - t0 <= kWaitLimitNs);
+  do {
+    if (mbar_try_wait(bar, parity)) return true;
+  } while (static_cast<uint32_t>(clock()) - t0 < kRwWaitClocks);
   return false;
 }
 __device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -139,30 +176,26 @@ __device__ __forceinline__ bool row_wait(uint64_t* bar, uint32_t parity, volatil
   return false;
 }
 
+// True in one lane of a converged warp. Products and commits stand under this, inside code that the
+// whole warp runs, so that their descriptors stay in uniform registers: behind `lane == 0` every
+// product took ~85 cycles to issue, with the tensor pipe needing 64.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// row_wait by a whole warp, with one answer.
+__device__ __forceinline__ bool row_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, row_wait(bar, parity, abort_flag));
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
 // n low bits set (n <= 0: none, n >= 32: all).
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-}
-
-// Lane L's tokens of an item, and the tiles it works on: the i-th is tile0 + first + i step.
-struct LaneView {
-  int nt, kend, used, first, step;
-};
-__device__ __forceinline__ LaneView lane_view(const RowItem& it, int lane_no, int tpt, bool causal) {
-  LaneView v;
-  const int at = it.alt ? 0 : lane_no * tpt;
-  v.nt = it.alt ? it.nt : max(0, min(tpt, it.nt - at));
-  v.kend = causal ? it.t0 + at + v.nt : it.k1;
-  if (it.alt) {
-    v.used = (it.ntile + 1 - lane_no) >> 1;
-    v.first = lane_no;
-    v.step = 2;
-  } else {
-    v.used = v.nt > 0 ? max(0, min(it.ntile, ((v.kend + 127) >> 7) - it.tile0)) : 0;
-    v.first = 0;
-    v.step = 1;
-  }
-  return v;
 }
 
 // The 32-key visibility words of one row in a key tile (bit i of word c: key 128 tile + 32 c + i).
@@ -200,32 +233,33 @@ __global__ void __launch_bounds__(kRwThreads, 1)
   constexpr int kHalves = Smem::kHalves, kStages = Smem::kStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, and known to be
   const int tpt = rows_tile_tokens(p.g);
 
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&S.full[s], 1);
-      mbar_init(&S.empty[s], 2);  // both lanes' issuers
+      mbar_init(&S.empty[s], 2);  // both lanes' products
     }
     for (int i = 0; i < kRwItems; ++i) {
       mbar_init(&S.ifull[i], 1);
-      mbar_init(&S.iempty[i], 8 + 4 + 2);  // softmax and epilogue warps, issuers
+      mbar_init(&S.iempty[i], 8 + 4 + 1);  // softmax and epilogue warps, the issuer
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.qfull[i], 1);
       mbar_init(&S.qempty[i], 1);
       mbar_init(&S.sfull[i], 1);
-      mbar_init(&S.pfull[i], 4);
-      mbar_init(&S.pvdone[i], 1);
+      mbar_init(&S.pfull[i][0], 4);
+      mbar_init(&S.pfull[i][1], 4);
       mbar_init(&S.ofin[i], 1);
       mbar_init(&S.oempty[i], 4);
       for (int j = 0; j < 2; ++j) {
         mbar_init(&S.lready[i][j], 4);
         mbar_init(&S.lfree[i][j], 4);
       }
-      mbar_init(&S.drain[i], 1);
     }
+    mbar_init(&S.drain, 1);
     S.abort_flag = 0;
     S.bad = 0;
     fence_mbar_init();
@@ -341,112 +375,136 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           const int mid = (u + hi) >> 1;
           if (a + rows_weight(kCausal, tpt, keys, mid) <= x0) u = mid; else hi = mid;
         }
+        // The next piece of this CTA's stretch into the item ring (slot K), or the stop mark. The
+        // consumers get it long before its tiles: planning takes this warp ~2500 cycles.
+        bool more = true;
+        auto publish = [&](uint32_t K_) -> bool {
+          const int slot = K_ & (kRwItems - 1);
+          if (!row_wait(&S.iempty[slot], ((K_ / kRwItems) & 1u) ^ 1u, &S.abort_flag)) return false;
+          RowItem& it = S.item[slot];
+          bool found = false;
+          while (more && !found) {
+            const int64_t a0 = a + rows_weight(kCausal, tpt, keys, u);
+            if (a0 >= x1) break;
+            const int64_t w = a + rows_weight(kCausal, tpt, keys, u + 1) - a0;
+            const int k1 = rows_item_keys(kCausal, tpt, n, keys, u);
+            const int tiles = (k1 + 127) >> 7;
+            const int c0 = rows_cut(x0, a0, w, tiles), c1 = rows_cut(x1, a0, w, tiles);
+            if (c0 < c1) {
+              found = true;
+              int cut0 = 0, cuts = 0;
+              if (c0 > 0 || c1 < tiles) rows_cuts(weight, nact, a0, w, tiles, cta, &cut0, &cuts);
+              const int t0 = u * 2 * tpt, nt = min(2 * tpt, n - t0);
+              const bool alt = nt <= tpt;
+              if (lane == 0) {
+                it.stop = 0;
+                it.b = b;
+                it.h = h;
+                it.t0 = t0;
+                it.row0 = static_cast<int>(row) + t0;
+                it.key_row0 = static_cast<int>(row);
+                it.tile0 = c0;
+                it.ntile = c1 - c0;
+                it.k1 = k1;
+                it.prefix = prefix;
+                it.alt = alt;
+                it.cut0 = cut0;
+                it.cuts = cuts;
+                it.piece = cuts > 0 ? cta + 1 - cut0 : 0;
+              }
+              if (lane < 2) {
+                const int first = alt ? 0 : lane * tpt, tokens = alt ? nt : min(tpt, nt - first);
+                const int kend = (kCausal ? t0 + first + tokens : k1) - c0 * 128;
+                it.tokens[lane] = tokens;
+                it.kend[lane] = kend;
+                it.used[lane] = alt ? (c1 - c0 + 1 - lane) >> 1 : max(0, min(c1 - c0, (kend + 127) >> 7));
+              }
+            }
+            if (++u == pairs) {
+              u = 0;
+              a += per_head;
+              if (++h == p.hkv) {
+                h = 0;
+                base += all;
+                row += n;
+                do {  // the next request with rows
+                  if (++b >= p.batch) break;
+                  request(b, &n, &keys, &prefix);
+                } while (n == 0);
+                more = b < p.batch;
+                if (more) {
+                  pairs = rows_pairs(n, tpt);
+                  per_head = rows_weight(kCausal, tpt, keys, pairs);
+                  all = p.hkv * per_head;
+                  a = base;
+                }
+              }
+            }
+          }
+          if (!found && lane == 0) it.stop = 1;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.ifull[slot]);
+          return true;
+        };
+        // one box a lane: its page and half of the tile (paged), or its half
+        const int psz = kSrc == kSrcPaged ? min(p.page_size, 128) : 128;
+        const int boxes = (128 / psz) * kHalves, box_page = lane / kHalves, box_half = lane % kHalves;
+        ok = publish(0);
         while (ok) {
-          const int64_t a0 = a + rows_weight(kCausal, tpt, keys, u);
-          if (a0 >= x1) break;
-          const int64_t w = a + rows_weight(kCausal, tpt, keys, u + 1) - a0;
-          const int k1 = rows_item_keys(kCausal, tpt, n, keys, u);
-          const int tiles = (k1 + 127) >> 7;
-          const int c0 = rows_cut(x0, a0, w, tiles), c1 = rows_cut(x1, a0, w, tiles);
-          if (c0 < c1) {
-            // ---- one piece: its descriptor, K of its first tile, Q, the rest ----
-            RowItem it;
-            it.stop = 0;
-            it.b = b;
-            it.h = h;
-            it.t0 = u * 2 * tpt;
-            it.nt = min(2 * tpt, n - it.t0);
-            it.row0 = static_cast<int>(row) + it.t0;
-            it.key_row0 = static_cast<int>(row);
-            it.tile0 = c0;
-            it.ntile = c1 - c0;
-            it.k1 = k1;
-            it.prefix = prefix;
-            it.alt = it.nt <= tpt;
-            it.cut0 = it.cuts = it.piece = 0;
-            if (c0 > 0 || c1 < tiles) {
-              rows_cuts(weight, nact, a0, w, tiles, cta, &it.cut0, &it.cuts);
-              it.piece = cta + 1 - it.cut0;
+          const RowItem& it = S.item[K & (kRwItems - 1)];
+          if (it.stop) break;
+          const int c0 = it.tile0, c1 = it.tile0 + it.ntile, k1 = it.k1, ih = it.h, ib = it.b;
+          const int key_row0 = it.key_row0, q_row = it.row0, q_step = it.alt ? 0 : tpt;
+          auto page_of = [&](int tile) -> int {
+            if constexpr (kSrc == kSrcPaged) {
+              const int key = tile * 128 + box_page * psz;
+              if (lane < boxes && key < k1) {
+                const int id = p.block_table[static_cast<int64_t>(ib) * p.pages_per_seq + key / p.page_size];
+                if (id >= 0 && id < p.num_pages) return id;
+                atomicOr(&p.hdr->status, FD_FLAG_BAD_PAGE);
+              }
+              return p.num_pages;  // outside the map: the copy writes zeros
             }
-            const int slot = K & (kRwItems - 1);
-            if (!row_wait(&S.iempty[slot], ((K / kRwItems) & 1u) ^ 1u, &S.abort_flag)) { ok = false; break; }
-            if (lane == 0) {
-              S.item[slot] = it;
-              mbar_arrive(&S.ifull[slot]);
-            }
+            return 0;
+          };
+          auto load = [&](const CUtensorMap* map, uint32_t c, int tile, int page) -> bool {
+            const int st = c % kStages;
+            if (!row_wait(&S.empty[st], ((c / kStages) & 1u) ^ 1u, &S.abort_flag)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(&S.full[st], kHalves * 128u * static_cast<uint32_t>(p.kv_box_rows * (128 / psz)));
             __syncwarp();
-            // where a tile's keys lie: this lane's box (paged), else all of the tile (lane 0)
-            const int psz = kSrc == kSrcPaged ? min(p.page_size, 128) : 128;
-            const int boxes = kSrc == kSrcPaged ? (128 / psz) * kHalves : kHalves;
-            const int box_page = lane / kHalves, box_half = lane % kHalves;
-            auto page_of = [&](int tile) -> int {
-              if constexpr (kSrc == kSrcPaged) {
-                const int key = tile * 128 + box_page * psz;
-                if (lane < boxes && key < k1) {
-                  const int id = p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + key / p.page_size];
-                  if (id >= 0 && id < p.num_pages) return id;
-                  atomicOr(&p.hdr->status, FD_FLAG_BAD_PAGE);
-                }
-                return p.num_pages;  // outside the map: the copy writes zeros
-              }
-              return 0;
-            };
-            auto load = [&](const CUtensorMap* map, uint32_t c, int tile, int page) -> bool {
-              const int st = c % kStages;
-              if (!row_wait(&S.empty[st], ((c / kStages) & 1u) ^ 1u, &S.abort_flag)) return false;
-              if (lane == 0) mbar_arrive_expect_tx(&S.full[st], kHalves * 128u * static_cast<uint32_t>(p.kv_box_rows * (128 / psz)));
-              __syncwarp();
-              if (lane < boxes) {
-                __nv_bfloat16* dst = S.kv[st][box_half] + box_page * psz * 64;
-                if constexpr (kSrc == kSrcPacked) tma_load_3d(dst, map, &S.full[st], 64 * box_half, h, it.key_row0 + tile * 128);
-                else if constexpr (kSrc == kSrcCache) tma_load_4d(dst, map, &S.full[st], 64 * box_half, tile * 128, h, b);
-                else tma_load_4d(dst, map, &S.full[st], 64 * box_half, tile * 128 % p.page_size, h, page);
-              }
-              return true;
-            };
-            int page = page_of(c0);
-            for (int j = c0; ok && j < c1; ++j, ++T) {
-              if (!load(&tmap_k, 2 * T, j, page)) { ok = false; break; }
-              if (j == c0) {
-                for (int L = 0; ok && L < 2; ++L) {
-                  if (!row_wait(&S.qempty[L], (K & 1u) ^ 1u, &S.abort_flag)) { ok = false; break; }
-                  if (lane == 0) mbar_arrive_expect_tx(&S.qfull[L], kHalves * 128u * static_cast<uint32_t>(p.g * p.q_box_rows));
-                  __syncwarp();
-                  if (lane < kHalves)
-                    tma_load_3d(S.q[L][lane], &tmap_q, &S.qfull[L], 64 * lane, h * p.g, it.row0 + (it.alt ? 0 : L * tpt));
-                }
-                if (!ok) break;
-              }
-              if (!load(&tmap_v, 2 * T + 1, j, page)) { ok = false; break; }
-              if (j + 1 < c1) page = page_of(j + 1);
+            if (lane < boxes) {
+              __nv_bfloat16* dst = S.kv[st][box_half] + box_page * psz * 64;
+              if constexpr (kSrc == kSrcPacked) tma_load_3d(dst, map, &S.full[st], 64 * box_half, ih, key_row0 + tile * 128);
+              else if constexpr (kSrc == kSrcCache) tma_load_4d(dst, map, &S.full[st], 64 * box_half, tile * 128, ih, ib);
+              else tma_load_4d(dst, map, &S.full[st], 64 * box_half, tile * 128 % p.page_size, ih, page);
             }
-            ++K;
-          }
-          if (++u == pairs) {
-            u = 0;
-            a += per_head;
-            if (++h == p.hkv) {
-              h = 0;
-              base += all;
-              row += n;
-              do {  // the next request with rows
-                if (++b >= p.batch) break;
-                request(b, &n, &keys, &prefix);
-              } while (n == 0);
-              if (b >= p.batch) break;
-              pairs = rows_pairs(n, tpt);
-              per_head = rows_weight(kCausal, tpt, keys, pairs);
-              all = p.hkv * per_head;
-              a = base;
+            return true;
+          };
+          int page = page_of(c0);
+#pragma unroll 1
+          for (int j = c0; j < c1; ++j, ++T) {
+            if (!load(&tmap_k, 2 * T, j, page)) { ok = false; break; }
+            if (j == c0) {
+#pragma unroll 1
+              for (int L = 0; L < 2; ++L) {
+                if (!row_wait(&S.qempty[L], (K & 1u) ^ 1u, &S.abort_flag)) { ok = false; break; }
+                if (lane == 0) mbar_arrive_expect_tx(&S.qfull[L], kHalves * 128u * static_cast<uint32_t>(p.g * p.q_box_rows));
+                __syncwarp();
+                if (lane < kHalves) tma_load_3d(S.q[L][lane], &tmap_q, &S.qfull[L], 64 * lane, ih * p.g, q_row + L * q_step);
+              }
+              if (!ok) break;
             }
+            if (!load(&tmap_v, 2 * T + 1, j, page)) { ok = false; break; }
+            if (j + 1 < c1) page = page_of(j + 1);
+            // the ring holds two tiles: plan while they are worked on
+            if (j == min(c0 + 1, c1 - 1) && !(ok = publish(K + 1))) break;
           }
+          if (ok) ++K;
         }
-      }
-      if (ok) {
-        const int slot = K & (kRwItems - 1);
-        if (row_wait(&S.iempty[slot], ((K / kRwItems) & 1u) ^ 1u, &S.abort_flag) && lane == 0) {
-          S.item[slot].stop = 1;
-          mbar_arrive(&S.ifull[slot]);
+      } else {
+        if (lane == 0) {
+          S.item[0].stop = 1;
+          mbar_arrive(&S.ifull[0]);
         }
       }
       __syncwarp();
@@ -460,78 +518,211 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           (void)row_poll(&S.qfull[L], K & 1u);
         }
       }
-    } else if (warp < kRwIssue + 2 && lane == 0) {
-      // ======================= tensor-core issue of one lane =======================
-      const int L = warp - kRwIssue;
-      const uint32_t s_col = tmem + 128 * L, o_col = tmem + kRwColO + kD * L;
+    } else if (warp == kRwIssue) {
+      // ======================= tensor-core issue =======================
+      // Step T of the key tiles: for each lane that uses tile T the product P·V of the lane's previous
+      // tile, then the scores of tile T over the same columns (products of one thread run in the
+      // order of their issue). The lanes' pairs of products alternate, so that one lane's softmax
+      // runs beside the other lane's products: with a thread a lane the commits queued behind the
+      // other lane's products, both softmaxes ran at once and a tile took 4830 cycles.
       const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
       const uint32_t idesc_o = idesc_bf16_f32(128, kD, false, true);
-      const uint64_t qd0 = smem_desc(smem_u32(S.q[L][0]), 16, 1024, kLayoutSW128);
-      uint32_t T = 0, J = 0;  // key tiles of the items so far; tiles this lane has used
+      const uint64_t q_desc = smem_desc(smem_u32(S.q[0][0]), 16, 1024, kLayoutSW128);
+      const uint64_t k_desc = smem_desc(smem_u32(S.kv[0][0]), 16, 1024, kLayoutSW128);
+      const uint64_t v_desc = smem_desc(smem_u32(S.kv[0][0]), kRwHalf, 1024, kLayoutSW128);
+      constexpr uint32_t kStageDesc = kHalves * (kRwHalf >> 4);  // a stage in the start-address field
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      // A lane's state (both lanes' stay in registers: every use names its lane at compile time).
+      struct Turn {
+        uint32_t pend = 0;      // 1 + the tile count T of the scores whose product is still to issue
+        uint32_t steps = 0;     // its key steps of 16
+        uint32_t J = 0;         // tiles of the lane so far
+        int first = 0, last = 0;  // the pending tile is its item's first (2 + a parity) / last
+        bool alone = false;       // the other lane does not use it
+        int i = 0, used = 0, next = 0, step = 1, kend = 0;  // this item: tiles done, all, the next one
+      } st0, st1;
+      uint32_t T = 0;
       bool ok = true;
+      auto product = [&](auto lane_no, Turn& st) -> bool {  // P·V of the lane's pending tile
+        constexpr int L = decltype(lane_no)::value;
+        const uint32_t cv = 2 * (st.pend - 1) + 1, sv = cv % kStages;
+        st.pend = 0;
+        if (!row_wait_warp(&S.full[sv], (cv / kStages) & 1u, &S.abort_flag)) return false;
+        if (st.first != 0 && !row_wait_warp(&S.oempty[L], st.first & 1u, &S.abort_flag)) return false;
+        const uint32_t s_col = tm + 128 * L, o_col = tm + kRwColO + kD * L;
+        const uint64_t vd = v_desc + static_cast<uint64_t>(sv * kStageDesc);
+        const uint32_t acc = st.first != 0 ? 0u : 1u;
+#pragma unroll 1
+        for (uint32_t half = 0; half < 2; ++half) {
+          if (!row_wait_warp(&S.pfull[L][half], (st.J - 1) & 1u, &S.abort_flag)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll 1
+            for (uint32_t kk = 4 * half; kk < min(st.steps, 4 * half + 4); ++kk)
+              umma_bf16_ts(o_col, s_col + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, kk > 0 ? 1u : acc);
+          }
+          __syncwarp();
+        }
+        if (elect_one()) {
+          umma_commit(&S.empty[sv]);
+          if (st.alone) umma_commit(&S.empty[sv]);
+          if (st.last != 0) umma_commit(&S.ofin[L]);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto turn = [&](auto lane_no, Turn& st, uint32_t K, int j, bool use, bool other) -> bool {
+        constexpr int L = decltype(lane_no)::value;
+        // an unused tile: only a product two tiles back, whose stage the next V tile needs
+        if (!use) return st.pend == 0 || st.pend + 1 > T || product(lane_no, st);
+        if (st.pend != 0 && !product(lane_no, st)) return false;
+        const uint32_t ck = 2 * T, sk = ck % kStages;
+        if (!row_wait_warp(&S.full[sk], (ck / kStages) & 1u, &S.abort_flag)) return false;
+        if (st.i == 0 && !row_wait_warp(&S.qfull[L], K & 1u, &S.abort_flag)) return false;
+        tc_fence_after();
+        const uint64_t qd = q_desc + static_cast<uint64_t>(L * kStageDesc), kd = k_desc + static_cast<uint64_t>(sk * kStageDesc);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kD / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kRwHalf >> 4) + (kk & 3) * 2);
+            umma_bf16_ss(tm + 128 * L, qd + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&S.sfull[L]);  // the softmax gives K's stage back
+        }
+        __syncwarp();
+        st.pend = T + 1;
+        // key steps of 16 up to the lane's last visible key
+        st.steps = static_cast<uint32_t>(min(128, st.kend - j * 128) + 15) >> 4;
+        st.first = st.i == 0 ? 2 + static_cast<int>((K & 1u) ^ 1u) : 0;
+        st.last = ++st.i == st.used;
+        st.alone = !other;
+        if (st.last != 0 && elect_one()) umma_commit(&S.qempty[L]);
+        st.next += st.step;
+        ++st.J;
+        return true;
+      };
+      // an item that gives the lane nothing to do: its Q goes back unread, its (empty) O is there
+      auto skip = [&](auto lane_no, Turn& st, uint32_t K) -> bool {
+        constexpr int L = decltype(lane_no)::value;
+        if (st.used != 0) return true;
+        if (!row_wait_warp(&S.qfull[L], K & 1u, &S.abort_flag)) return false;
+        if (lane == 0) mbar_arrive(&S.qempty[L]);
+        if (st.pend != 0 && !product(lane_no, st)) return false;
+        if (!row_wait_warp(&S.oempty[L], (K & 1u) ^ 1u, &S.abort_flag)) return false;
+        if (lane == 0) mbar_arrive(&S.ofin[L]);
+        return true;
+      };
+      constexpr std::integral_constant<int, 0> lane0{};
+      constexpr std::integral_constant<int, 1> lane1{};
       for (uint32_t K = 0; ok; ++K) {
         const int slot = K & (kRwItems - 1);
-        if (!row_wait(&S.ifull[slot], (K / kRwItems) & 1u, &S.abort_flag)) break;
-        const RowItem it = S.item[slot];
-        mbar_arrive(&S.iempty[slot]);
-        if (it.stop) break;
-        const LaneView v = lane_view(it, L, tpt, kCausal);
-        if (!row_wait(&S.qfull[L], K & 1u, &S.abort_flag)) break;
-        if (v.used == 0) mbar_arrive(&S.qempty[L]);
-        int i = 0;  // tiles used of this item
-        for (int j = 0; j < it.ntile; ++j, ++T) {
-          const uint32_t ck = 2 * T, cv = 2 * T + 1;
-          const int sk = ck % kStages, sv = cv % kStages;
-          const bool use = i < v.used && j == v.first + i * v.step;
-          if (!row_wait(&S.full[sk], (ck / kStages) & 1u, &S.abort_flag)) { ok = false; break; }
-          if (use) {
-            // S and P share their columns: the product that read the last P is done
-            if (J > 0 && !row_wait(&S.pvdone[L], (J - 1) & 1u, &S.abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            const uint64_t kd0 = smem_desc(smem_u32(S.kv[sk][0]), 16, 1024, kLayoutSW128);
+        if (!row_wait_warp(&S.ifull[slot], (K / kRwItems) & 1u, &S.abort_flag)) { ok = false; break; }
+        const RowItem& it = S.item[slot];
+        const auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+        if (uniform(it.stop)) break;
+        const int ntile = uniform(it.ntile), alt = uniform(it.alt);
+        auto begin = [&](int L, Turn& st) {
+          st.i = 0;
+          st.used = uniform(it.used[L]);
+          st.next = alt ? L : 0;
+          st.step = alt ? 2 : 1;
+          st.kend = uniform(it.kend[L]);
+        };
+        begin(0, st0);
+        begin(1, st1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.iempty[slot]);
+        // Tiles [2, plain) of a two-tile item: both lanes use them, neither the product of the tile before
+        // nor the scores are an item's first or last. The general turns below cost the issuing warp
+        // ~600 cycles of bookkeeping each, which left the tensor pipe idle as long.
+        const int plain = st0.step == 1 ? st0.used - 1 : 0;
+        for (int j = 0; ok && j < ntile; ++j, ++T) {
+          if (j == 2 && plain > 2) {
+            uint32_t sk = 2 * T % kStages, pk = (2 * T / kStages) & 1u;          // K of tile T
+            uint32_t sv = (2 * T - 1) % kStages, pv = ((2 * T - 1) / kStages) & 1u;  // V of tile T - 1
+            uint32_t p0 = (st0.J - 1) & 1u, p1 = (st1.J - 1) & 1u;
+            const int n = plain - 2;
+            for (int i = 0; i < n; ++i) {
+              const uint64_t kd = k_desc + static_cast<uint64_t>(sk * kStageDesc), vd = v_desc + static_cast<uint64_t>(sv * kStageDesc);
+              ok = row_wait_warp(&S.full[sv], pv, &S.abort_flag) && row_wait_warp(&S.full[sk], pk, &S.abort_flag) &&
+                   row_wait_warp(&S.pfull[0][0], p0, &S.abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kD / 16; ++kk) {
-              const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kRwHalf >> 4) + (kk & 3) * 2);
-              umma_bf16_ss(s_col, qd0 + off, kd0 + off, idesc_s, kk > 0 ? 1u : 0u);
-            }
-            umma_commit(&S.sfull[L]);
-            umma_commit(&S.empty[sk]);
-            if (i == v.used - 1) umma_commit(&S.qempty[L]);
-          } else {
-            mbar_arrive(&S.empty[sk]);
-          }
-          if (!row_wait(&S.full[sv], (cv / kStages) & 1u, &S.abort_flag)) { ok = false; break; }
-          if (use) {
-            if (i == 0 && !row_wait(&S.oempty[L], (K & 1u) ^ 1u, &S.abort_flag)) { ok = false; break; }
-            if (!row_wait(&S.pfull[L], J & 1u, &S.abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            // key steps of 16 up to the lane's last visible key
-            const int steps = (min(128, min(it.k1, v.kend) - (it.tile0 + j) * 128) + 15) >> 4;
-            const uint64_t vd0 = smem_desc(smem_u32(S.kv[sv][0]), kRwHalf, 1024, kLayoutSW128);
-            if (steps == 8) {
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16_ts(tm + kRwColO, tm + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
+              }
+              ok = row_wait_warp(&S.pfull[0][1], p0, &S.abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_bf16_ts(o_col, s_col + 8 * kk, vd0 + static_cast<uint64_t>(kk * 128), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
-            } else {
-              for (int kk = 0; kk < steps; ++kk)
-                umma_bf16_ts(o_col, s_col + 8 * kk, vd0 + static_cast<uint64_t>(kk * 128), idesc_o, (i > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 4; kk < 8; ++kk)
+                  umma_bf16_ts(tm + kRwColO, tm + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
+#pragma unroll
+                for (int kk = 0; kk < kD / 16; ++kk) {
+                  const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kRwHalf >> 4) + (kk & 3) * 2);
+                  umma_bf16_ss(tm, q_desc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&S.sfull[0]);
+              }
+              __syncwarp();
+              ok = row_wait_warp(&S.pfull[1][0], p1, &S.abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16_ts(tm + kRwColO + kD, tm + 128 + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
+              }
+              ok = row_wait_warp(&S.pfull[1][1], p1, &S.abort_flag);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 4; kk < 8; ++kk)
+                  umma_bf16_ts(tm + kRwColO + kD, tm + 128 + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
+                umma_commit(&S.empty[sv]);
+                umma_commit(&S.empty[sv]);
+#pragma unroll
+                for (int kk = 0; kk < kD / 16; ++kk) {
+                  const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kRwHalf >> 4) + (kk & 3) * 2);
+                  umma_bf16_ss(tm + 128, q_desc + kStageDesc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&S.sfull[1]);
+              }
+              __syncwarp();
+              if ((sk += 2) >= kStages) { sk -= kStages; pk ^= 1u; }
+              if ((sv += 2) >= kStages) { sv -= kStages; pv ^= 1u; }
+              p0 ^= 1u;
+              p1 ^= 1u;
             }
-            umma_commit(&S.pvdone[L]);
-            umma_commit(&S.empty[sv]);
-            if (i == v.used - 1) umma_commit(&S.ofin[L]);
-            ++i;
-            ++J;
-          } else {
-            mbar_arrive(&S.empty[sv]);
+            if (!ok) break;
+            j += n;
+            T += n;
+            auto forward = [&](Turn& st) {
+              st.pend = T;
+              st.steps = 8;
+              st.first = st.last = 0;
+              st.alone = false;
+              st.i += n;
+              st.next += n;
+              st.J += n;
+            };
+            forward(st0);
+            forward(st1);
           }
+          const bool use0 = st0.i < st0.used && j == st0.next, use1 = st1.i < st1.used && j == st1.next;
+          ok = turn(lane0, st0, K, j, use0, use1) && turn(lane1, st1, K, j, use1, use0);
         }
-        if (ok && v.used == 0) {
-          if (!row_wait(&S.oempty[L], (K & 1u) ^ 1u, &S.abort_flag)) break;
-          mbar_arrive(&S.ofin[L]);
-        }
+        ok = ok && skip(lane0, st0, K) && skip(lane1, st1, K);
       }
-      umma_commit(&S.drain[L]);
-      (void)row_poll(&S.drain[L], 0);
+      if (ok && st0.pend != 0) ok = product(lane0, st0);
+      if (ok && st1.pend != 0) ok = product(lane1, st1);
+      if (elect_one()) umma_commit(&S.drain);
+      __syncwarp();
+      (void)row_poll(&S.drain, 0);
     }
     __syncwarp();
   } else if (warp < kRwEpi) {
@@ -550,15 +741,16 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       if (!row_wait(&S.ifull[slot], (K / kRwItems) & 1u, &S.abort_flag)) break;
       const RowItem& it = S.item[slot];  // stays in shared memory: the scores need the registers
       if (it.stop) break;
-      const LaneView v = lane_view(it, L, tpt, kCausal);
-      const int pos = pos_in + (it.alt ? 0 : L * tpt);  // token of the item
-      const bool row_ok = pos_in < v.nt;
+      const int used = it.used[L], alt = it.alt;
+      const int both = alt ? 0 : it.used[0];        // tiles that both lanes use
+      const int pos = pos_in + (alt ? 0 : L * tpt);  // token of the item
+      const bool row_ok = pos_in < it.tokens[L];
       float m = -INFINITY;
       uint64_t sum2[4];
 #pragma unroll
       for (int a = 0; a < 4; ++a) sum2[a] = 0;
-      for (int i = 0; i < v.used; ++i, ++J) {
-        const int j = v.first + i * v.step, tile = it.tile0 + j;
+      for (int i = 0; i < used; ++i, ++J) {
+        const int j = alt ? 2 * i + L : i, tile = it.tile0 + j;
         uint32_t w[4];
         // tiles that every row of this warp sees whole need no mask
         bool full;
@@ -567,6 +759,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         if (!full) visible_words<kCausal>(p, it, tile, pos, row_ok, static_cast<int64_t>(it.row0) + pos, w);
         if (!row_wait(&S.sfull[L], J & 1u, &S.abort_flag)) { ok = false; break; }
         tc_fence_after();
+        // K of this tile is no longer read (its stage expects two arrivals; a tile of one lane gives both)
+        if (warp == 4 * L && lane == 0) mbar_arrive_n(&S.empty[2 * (T + j) % kStages], i < both ? 1u : 2u);
         uint32_t x[128];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
@@ -577,14 +771,14 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         }
         float mx[4];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) mx[a] = fmaxf(__uint_as_float(x[2 * a]), __uint_as_float(x[2 * a + 1]));
+        for (int a = 0; a < 4; ++a) mx[a] = max3_f32(__uint_as_float(x[2 * a]), __uint_as_float(x[2 * a + 1]), -INFINITY);
 #pragma unroll
         for (int e = 8; e < 128; e += 8)
 #pragma unroll
           for (int a = 0; a < 4; ++a)
             mx[a] = max3_f32(mx[a], __uint_as_float(x[e + 2 * a]), __uint_as_float(x[e + 2 * a + 1]));
-        const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
-        const bool move = mn > m + kRwRescale || (m == -INFINITY && mn != -INFINITY);
+        const float mn = max3_f32(m, max3_f32(max3_f32(mx[0], mx[1], mx[2]), mx[3], -INFINITY) * p.scale_log2, -INFINITY);
+        const bool move = !(mn <= m + kRwRescale);  // from -inf, and for NaN too
         if (i > 0 && __any_sync(0xffffffffu, move)) {
           // the scores of this tile were issued after the last product into O had completed
           const float alpha = move ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
@@ -602,22 +796,9 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           for (int a = 0; a < 4; ++a) sum2[a] = fma_f32x2(sum2[a], alpha2, 0ull);
         }
         if (move) m = mn;
-        const float negm = m == -INFINITY ? 0.f : -m;  // then every score is -inf
+        // -m; 0 where every score is -inf so far, NaN for a row that saw +inf (as for one that saw NaN)
+        const float negm = m == -INFINITY ? 0.f : fmaf(m, 0.f, -m);
         const uint64_t negm2 = pair_f32(negm, negm);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t out[16];
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float a0, a1;
-            unpair_f32(fma_f32x2(pair_f32(__uint_as_float(x[32 * c + e]), __uint_as_float(x[32 * c + e + 1])), scale2, negm2), a0, a1);
-            a0 = fast_exp2(a0);
-            a1 = fast_exp2(a1);
-            out[e >> 1] = pack_bf16(a0, a1);
-            sum2[(e >> 1) & 3] = add_f32x2(sum2[(e >> 1) & 3], pair_f32(a0, a1));
-          }
-          tmem_st16(s_col + 16 * c, out);
-        }
         const int valid = it.k1 - tile * 128;
         if (valid < 128 && (valid & 15) != 0) {
           // zero V rows [valid, next multiple of 16): they may lie behind the request's keys
@@ -631,10 +812,37 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           }
           fence_proxy_async_smem();
         }
+        // P in two halves of 64 keys, so that the product with V starts before the second is done; a
+        // half is reported one 32-key step late, when its stores have long landed
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t out[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const uint64_t a = fma_f32x2(pair_f32(__uint_as_float(x[32 * c + e]), __uint_as_float(x[32 * c + e + 1])), scale2, negm2);
+            float a0, a1;
+            if ((e >> 1) % kRwPolyEvery == kRwPolyEvery - 1) {
+              exp2_poly(a, a0, a1);
+            } else {
+              unpair_f32(a, a0, a1);
+              a0 = fast_exp2(a0);
+              a1 = fast_exp2(a1);
+            }
+            out[e >> 1] = pack_bf16(a0, a1);
+            sum2[(e >> 1) & 3] = add_f32x2(sum2[(e >> 1) & 3], pair_f32(a0, a1));
+          }
+          if (c == 2) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.pfull[L][0]);
+          }
+          tmem_st16(s_col + 16 * c, out);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.pfull[L]);
+        if (lane == 0) mbar_arrive(&S.pfull[L][1]);
       }
       if (!ok) break;
       T += it.ntile;
@@ -646,7 +854,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       const uint32_t ob = K & 1;
       if (!row_wait(&S.lfree[ob][L], ((K >> 1) & 1u) ^ 1u, &S.abort_flag)) break;
       S.mfin[ob][L][r] = m;
-      S.lfin[ob][L][r] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+      // a row that saw no key has only the polynomial's 2^-126 in its sums
+      S.lfin[ob][L][r] = m == -INFINITY ? 0.f : ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.lready[ob][L]);
     }
@@ -667,22 +876,22 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       if (it.stop) break;
       const uint32_t ob = K & 1;
       const int tiles = it.alt ? 1 : 2;  // row tiles
-      // one row of the output (32 columns at a time) and its log-sum-exp
-      auto store = [&](int t, int c, const float (&o)[32], float inv) {
-        const int pos = pos_in + t * tpt;
-        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) + (static_cast<int64_t>(it.row0) + pos) * p.o_sr +
-                             static_cast<int64_t>(it.h * p.g + head_in) * p.o_sh + c;
+      // 32 columns of a row as 16 bf16 pairs, a row's 16 x kD / 32 pairs to memory, its log-sum-exp
+      auto pack = [&](const float (&o)[32], float inv, uint32_t* to) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(dst + e) = make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                                                          pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+        for (int e = 0; e < 16; ++e) to[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
       };
       auto store_lse = [&](int t, float m, float l) {
         p.lse[(static_cast<int64_t>(it.row0) + pos_in + t * tpt) * p.hq + it.h * p.g + head_in] =
-            l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      };
+      auto out_row = [&](int t) {
+        return reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
+                                        (static_cast<int64_t>(it.row0) + pos_in + t * tpt) * p.o_sr +
+                                        static_cast<int64_t>(it.h * p.g + head_in) * p.o_sh);
       };
       for (int t = 0; t < tiles; ++t) {
-        const bool row_ok = pos_in < min(tpt, it.nt - t * tpt);
+        const bool row_ok = pos_in < it.tokens[t];
         float m, l, f0 = 1.f, f1 = 0.f;  // O = f0 O_first + f1 O_second
         for (int L = t; L < (it.alt ? 2 : t + 1); ++L) {
           if (!row_wait(&S.lready[ob][L], (K >> 1) & 1u, &S.abort_flag)) { ok = false; break; }
@@ -703,43 +912,87 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         }
         if (!ok) break;
         tc_fence_after();
-        const bool seen0 = !(l <= 0.f) && f0 != 0.f, seen1 = f1 != 0.f;
-        const int part = 2 * static_cast<int>(blockIdx.x) + (it.piece > 0 ? 0 : 1);
-        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
-          float o[32];
-          {
-            uint32_t raw[32];
-            tmem_ld32(o_base + kD * t + c, raw);
+        // Columns c .. c + 31 of the row, times `scale`. A lane without tiles has left its accumulator
+        // as it was: that one is not looked at.
+        const bool none0 = it.used[t] == 0, none1 = it.used[1] == 0;
+        auto read = [&](int c, float scale, uint64_t (&o)[16]) {
+          uint32_t raw[32];
+          tmem_ld32(o_base + kD * t + c, raw);
+          tmem_wait_ld();
+          const float s0 = scale * f0, s1 = scale * f1;
+          const uint64_t s02 = pair_f32(s0, s0), s12 = pair_f32(s1, s1);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[e] = none0 ? 0ull : fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s02, 0ull);
+          if (it.alt && !none1) {
+            tmem_ld32(o_base + kD + c, raw);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = seen0 ? __uint_as_float(raw[e]) * f0 : 0.f;
-            if (it.alt) {
-              tmem_ld32(o_base + kD + c, raw);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = seen1 ? fmaf(__uint_as_float(raw[e]), f1, o[e]) : o[e];
-            }
+            for (int e = 0; e < 16; ++e)
+              o[e] = fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s12, o[e]);
           }
-          if (it.cuts == 0) {
-            if (row_ok) store(t, c, o, inv);
-          } else {
-            float4* dst = part_o + ((static_cast<int64_t>(part) * 2 + t) * (kD / 4) + c / 4) * 128 + r;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e * 128] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
-        }
+        };
         if (it.cuts == 0) {
+          // 64 columns at a time through shared memory, so that eight lanes store a row's 128 bytes:
+          // a thread storing its own row kept the load/store pipe, and with it every warp's barrier
+          // and tensor-memory traffic, busy for ~3000 cycles an item.
+          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll 1
+          for (int c0 = 0; c0 < kD; c0 += 64) {
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 32) {
+              uint64_t o[16];
+              uint32_t w[16];
+              read(c0 + c, inv, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float lo, hi;
+                unpair_f32(o[e], lo, hi);
+                w[e] = pack_bf16(lo, hi);
+              }
+              uint4* dst = reinterpret_cast<uint4*>(S.stage[quad][lane] + c * 2);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            }
+            if (c0 + 64 == kD) {  // the accumulator is read: the next item's first product may start
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(&S.oempty[t]);
+                if (it.alt) mbar_arrive(&S.oempty[1]);
+              }
+            }
+            __syncwarp();
+#pragma unroll 2
+            for (int i = 0; i < 32; i += 4) {
+              const int row = i + (lane >> 3), rr = quad * 32 + row;
+              const int rpos = (rr * p.g_recip16) >> 16;
+              const uint4 x = *reinterpret_cast<const uint4*>(S.stage[quad][row] + (lane & 7) * 16);
+              if (rpos < it.tokens[t])
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
+                                          (static_cast<int64_t>(it.row0) + rpos + t * tpt) * p.o_sr +
+                                          static_cast<int64_t>(it.h * p.g + rr - rpos * p.g) * p.o_sh + c0 + (lane & 7) * 8) = x;
+            }
+            __syncwarp();
+          }
           if (row_ok) store_lse(t, m, l);
         } else {
+          const int part = 2 * static_cast<int>(blockIdx.x) + (it.piece > 0 ? 0 : 1);
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 32) {
+            uint64_t o[16];
+            read(c, 1.f, o);
+            ulonglong2* dst = reinterpret_cast<ulonglong2*>(part_o) + ((static_cast<int64_t>(part) * 2 + t) * (kD / 4) + c / 4) * 128 + r;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e * 128] = make_ulonglong2(o[2 * e], o[2 * e + 1]);
+          }
           part_ml[(static_cast<int64_t>(part) * 2 + t) * 128 + r] = make_float2(m, l);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&S.oempty[t]);
-          if (it.alt) mbar_arrive(&S.oempty[1]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&S.oempty[t]);
+            if (it.alt) mbar_arrive(&S.oempty[1]);
+          }
         }
       }
       if (!ok) break;
@@ -756,7 +1009,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           if (lane == 0) atomicSub(counter, static_cast<uint32_t>(it.cuts + 1) << (8 * quad));
           auto piece_slot = [&](int q) { return 2 * (it.cut0 - 1 + q) + (q > 0 ? 0 : 1); };
           for (int t = 0; t < tiles; ++t) {
-            const bool row_ok = pos_in < min(tpt, it.nt - t * tpt);
+            const bool row_ok = pos_in < it.tokens[t];
             float m = -INFINITY, l = 0.f;
             for (int q = 0; q <= it.cuts; ++q) {
               const float2 ml = __ldcg(part_ml + (static_cast<int64_t>(piece_slot(q)) * 2 + t) * 128 + r);
@@ -787,7 +1040,13 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                   o[4 * e + 3] = fmaf(f, y.w, o[4 * e + 3]);
                 }
               }
-              if (row_ok) store(t, c, o, inv);
+              if (row_ok) {
+                uint32_t w[16];
+                pack(o, inv, w);
+                uint4* dst = out_row(t) + c / 8;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+              }
             }
             if (row_ok) store_lse(t, m, l);
           }

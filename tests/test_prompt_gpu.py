@@ -99,10 +99,18 @@ def test_a_keys_non_finite_scores_reach_only_the_rows_that_see_it():
     q, k, v = _inputs([300], 8, 2, 128, 9)
     lens = torch.tensor([300], dtype=torch.int32, device="cuda")
     good = fd.fd_prompt_attention(q, k, v, lens)
-    k[200] = NAN
+    for value in (NAN, float("inf"), float("-inf")):
+        k[200] = value
+        bad = fd.fd_prompt_attention(q, k, v, lens)
+        for a, b in zip(good, bad):
+            assert torch.equal(a[:200], b[:200])
+            if value != value:
+                assert bool(b[200:].isnan().all())
+    k[200, :, 1:], k[200, :, 0] = 0.0, float("inf")  # scores of +inf or -inf by the sign of q's first element
     bad = fd.fd_prompt_attention(q, k, v, lens)
-    for a, b in zip(good, bad):
-        assert torch.equal(a[:200], b[:200])
+    up = q[200:, :, 0] > 0
+    assert bool(bad[0][200:][up].isnan().all()) and bool(bad[1][200:][up].isnan().all())
+    assert bool(bad[0][200:][~up].isfinite().all()) and bool(bad[1][200:][~up].isfinite().all())
 
 
 def test_bad_lengths():
