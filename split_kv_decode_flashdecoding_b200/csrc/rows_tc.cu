@@ -26,8 +26,8 @@
 // in the workspace and the last of its CTAs adds them in piece order, so results do not depend on
 // which one that is.
 //
-// Warps: 0-3 and 4-7 softmax of lanes 0 and 1 (warp w reads TMEM lanes 32 (w mod 4) + [0, 32), one row a
-// thread); 8-11 epilogue; 12 plan and TMA; 13 tensor-core issue.
+// Warps: 0-3 and 4-7 softmax and output of lanes 0 and 1 (warp w reads TMEM lanes 32 (w mod 4) + [0, 32),
+// one row a thread); 8 plan and TMA; 9 tensor-core issue.
 #include <type_traits>
 
 #include "common.cuh"
@@ -38,14 +38,13 @@ namespace fd {
 
 namespace {
 
-constexpr int kRwThreads = 16 * 32;
-constexpr int kRwEpi = 8, kRwProducer = 12, kRwIssue = 13;
+constexpr int kRwThreads = 12 * 32;
+constexpr int kRwProducer = 8, kRwIssue = 9;
 constexpr int kRwItems = 4;                    // item descriptors in flight
 constexpr uint32_t kRwTmemCols = 512;
 constexpr uint32_t kRwColO = 256;              // O of lane L at kRwColO + L D; S / P of lane L at 128 L
 constexpr uint32_t kRwHalf = 128 * 64 * 2;     // bytes of one 64-column half of a 128-row tile
 constexpr float kRwRescale = 8.0f;             // log2 units
-constexpr int kRwPolyEvery = 4;                // of a row's pairs of exponentials, one on the FMA pipe
 constexpr uint32_t kRwWaitClocks = 0x80000000u;
 
 enum RowSource { kSrcPacked = 0, kSrcCache = 1, kSrcPaged = 2 };
@@ -72,18 +71,18 @@ struct __align__(1024) RwSmem {
   __nv_bfloat16 q[2][kHalves][128 * 64];
   __nv_bfloat16 kv[kStages][kHalves][128 * 64];
   RowItem item[kRwItems];
-  float mfin[2][2][128], lfin[2][2][128];  // [item parity][lane][row]
+  float2 xend[8][32];  // softmax warps: a row's (m, l) at the end of an alt item, for the other lane's warp
   union {
     struct {  // plan: work, rows and items of a thread's requests
       int64_t part_w[kRwThreads];
       int32_t part_r[kRwThreads], part_i[kRwThreads];
     };
-    unsigned char stage[4][32][144];  // epilogue: 64 columns of a warp's rows, 16 bytes of padding each
+    uint4 stage[8][64];  // output: eight rows of 64 columns of a warp
   };
   uint64_t full[kStages], empty[kStages];
   uint64_t qfull[2], qempty[2], ifull[kRwItems], iempty[kRwItems];
   uint64_t sfull[2], pfull[2][2], ofin[2], oempty[2];  // pfull: keys [0, 64) and [64, 128)
-  uint64_t lready[2][2], lfree[2][2];
+  uint64_t xpair[4];  // exchanges of the two lanes' warps of a row quarter (alt items)
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -111,31 +110,6 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
-}
-// 2^x for a pair, x <= 2^7, on the FMA pipe: the special-function unit gives 16 exponentials a clock,
-// which is as long for a tile as its two products, so every kRwPolyEvery-th pair is computed here.
-// x = n + f with n the nearest integer (in the low bits of x + 1.5 2^23) and 2^f, |f| <= 1/2, by the
-// polynomial of degree 5 with the least relative error (Remez exchange; 7.5e-8, 2.1e-7 evaluated in
-// fp32: below the 2^-22 of the hardware's). x below -126 counts as -126.
-__device__ __forceinline__ void exp2_poly(uint64_t x, float& lo, float& hi) {
-  const uint64_t magic = pair_f32(12582912.f, 12582912.f), back = pair_f32(-12582912.f, -12582912.f);
-  float x0, x1;
-  unpair_f32(x, x0, x1);
-  x = pair_f32(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-  const uint64_t t = add_f32x2(x, magic);
-  const uint64_t n = add_f32x2(t, back);
-  const uint64_t f = fma_f32x2(n, pair_f32(-1.f, -1.f), x);
-  uint64_t y = pair_f32(1.3276472454890609e-3f, 1.3276472454890609e-3f);
-  y = fma_f32x2(y, f, pair_f32(9.675540961325169e-3f, 9.675540961325169e-3f));
-  y = fma_f32x2(y, f, pair_f32(5.550713092088699e-2f, 5.550713092088699e-2f));
-  y = fma_f32x2(y, f, pair_f32(2.4022120237350464e-1f, 2.4022120237350464e-1f));
-  y = fma_f32x2(y, f, pair_f32(6.931469440460205e-1f, 6.931469440460205e-1f));
-  y = fma_f32x2(y, f, pair_f32(1.0000001192092896f, 1.0000001192092896f));
-  float t0, t1, y0, y1;
-  unpair_f32(t, t0, t1);
-  unpair_f32(y, y0, y1);
-  lo = __uint_as_float(__float_as_uint(y0) + (__float_as_uint(t0) << 23));
-  hi = __uint_as_float(__float_as_uint(y1) + (__float_as_uint(t1) << 23));
 }
 // Maximum that a NaN wins, so that a row which sees one becomes NaN as a whole.
 __device__ __forceinline__ float max3_f32(float a, float b, float c) {
@@ -224,6 +198,145 @@ __device__ __forceinline__ void visible_words(const RowsParams& p, const RowItem
   }
 }
 
+// The end of an item for one softmax warp: columns c0 + [0, kW) of its 32 rows of row tile t (`last`:
+// its last ones), the accumulator(s) at o_base (an alt item: both lanes', times f0 and f1) over l, to memory; or, for a
+// piece of a cut item, unscaled to the workspace, where the warp that counts the last piece adds
+// them all in piece order. Rows leave through shared memory, eight at a time, so that neighbouring
+// threads store neighbouring bytes: a thread storing its own row kept the load/store pipe, and with
+// it every warp's barrier and tensor-memory traffic, busy for ~3000 cycles an item.
+template <int kD, int kW, bool kAlt, typename Smem>
+__device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const RowItem& it, int warp, int lane, int t,
+                                           int c0, bool last, uint32_t o_base, int tpt, float m, float l, float f0, float f1) {
+  constexpr int kUnits = kW / 8;  // 16-byte units of a row's columns
+  const int quad = warp & 3;
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  auto store = [&](const uint32_t (&w)[kW / 2], int c) {
+    uint4* stage = S.stage[warp];
+#pragma unroll 1
+    for (int g = 0; g < 4; ++g) {
+      __syncwarp();
+      if ((lane >> 3) == g) {
+#pragma unroll
+        for (int e = 0; e < kUnits; ++e)
+          stage[(lane & 7) * kUnits + (e ^ (lane & (kUnits - 1)))] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int n = lane; n < 8 * kUnits; n += 32) {
+        const int row = n / kUnits, e = n % kUnits;
+        const int rr = quad * 32 + g * 8 + row, pos = (rr * p.g_recip16) >> 16;
+        const uint4 v = stage[row * kUnits + (e ^ (row & (kUnits - 1)))];
+        if (pos < it.tokens[t])
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
+                                    (static_cast<int64_t>(it.row0) + pos + t * tpt) * p.o_sr +
+                                    static_cast<int64_t>(it.h * p.g + rr - pos * p.g) * p.o_sh + c + e * 8) = v;
+      }
+    }
+  };
+  auto store_lse = [&]() {
+    const int r = quad * 32 + lane, pos = (r * p.g_recip16) >> 16;
+    if (pos < it.tokens[t])
+      p.lse[(static_cast<int64_t>(it.row0) + pos + t * tpt) * p.hq + it.h * p.g + r - pos * p.g] =
+          l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  };
+  // A lane without tiles has left its accumulator as it was: that one is not looked at.
+  const bool none0 = it.used[kAlt ? 0 : t] == 0, none1 = it.used[1] == 0;
+  const float scale = it.cuts == 0 ? inv : 1.f;
+  const float s0 = scale * f0, s1 = scale * f1;
+  const uint64_t s02 = pair_f32(s0, s0), s12 = pair_f32(s1, s1);
+  uint64_t o[kW / 2];
+#pragma unroll
+  for (int c = 0; c < kW; c += 16) {
+    uint32_t raw[16];
+    tmem_ld16(o_base + c0 + c, raw);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      o[c / 2 + e] = none0 ? 0ull : fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s02, 0ull);
+    if (kAlt && !none1) {
+      tmem_ld16(o_base + kD + c0 + c, raw);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        o[c / 2 + e] = fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s12, o[c / 2 + e]);
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  if (last && lane == 0) {  // the accumulator is read: the next item's first product may start
+    mbar_arrive_n(&S.oempty[t], kAlt ? 1u : 2u);
+    if (kAlt) mbar_arrive_n(&S.oempty[1], 1u);
+  }
+  uint32_t w[kW / 2];
+  auto pack_all = [&]() {
+#pragma unroll
+    for (int e = 0; e < kW / 2; ++e) {
+      float lo, hi;
+      unpair_f32(o[e], lo, hi);
+      w[e] = pack_bf16(lo, hi);
+    }
+  };
+  if (it.cuts == 0) {
+    pack_all();
+    store(w, c0);
+    if (c0 == 0) store_lse();
+    return;
+  }
+  // pieces: O as [slot][row tile][D / 4][128 rows] float4, (m, l) as [slot][warp][32 rows] float2
+  ulonglong2* part_o = reinterpret_cast<ulonglong2*>(p.part_o);
+  float2* part_ml = reinterpret_cast<float2*>(p.part_ml);
+  const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (it.piece > 0 ? 0 : 1);
+  auto place = [&](int64_t slot, int c) { return ((slot * 2 + t) * (kD / 4) + c / 4) * 128 + quad * 32 + lane; };
+#pragma unroll
+  for (int e = 0; e < kW / 4; ++e) part_o[place(part, c0) + e * 128] = make_ulonglong2(o[2 * e], o[2 * e + 1]);
+  part_ml[(part * 8 + warp) * 32 + lane] = make_float2(m, l);
+  if (!last) return;
+  __threadfence();
+  __syncwarp();
+  uint32_t* counter = &p.hdr->row_pieces[it.cut0][warp >> 2];
+  uint32_t before = 0;
+  if (lane == 0) before = (atomicAdd(counter, 1u << (8 * quad)) >> (8 * quad)) & 0xffu;
+  before = __shfl_sync(0xffffffffu, before, 0);
+  if (before != static_cast<uint32_t>(it.cuts)) return;
+  __threadfence();
+  if (lane == 0) atomicSub(counter, static_cast<uint32_t>(it.cuts + 1) << (8 * quad));
+  auto piece_slot = [&](int q) { return 2 * static_cast<int64_t>(it.cut0 - 1 + q) + (q > 0 ? 0 : 1); };
+  m = -INFINITY;
+  for (int q = 0; q <= it.cuts; ++q) {
+    const float2 ml = __ldcg(part_ml + (piece_slot(q) * 8 + warp) * 32 + lane);
+    if (!(ml.y == 0.f)) m = fmaxf(m, ml.x);
+  }
+#pragma unroll 1
+  for (int c = kAlt ? c0 : 0; c <= c0; c += kW) {
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < kW / 2; ++e) o[e] = 0;
+#pragma unroll 1
+    for (int q = 0; q <= it.cuts; ++q) {
+      const ulonglong2* src = part_o + place(piece_slot(q), c);
+      ulonglong2 y[kW / 4];
+#pragma unroll
+      for (int e = 0; e < kW / 4; ++e) y[e] = __ldcg(src + e * 128);
+      const float2 ml = __ldcg(part_ml + (piece_slot(q) * 8 + warp) * 32 + lane);
+      const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      const uint64_t f2 = pair_f32(f, f);
+#pragma unroll
+      for (int e = 0; e < kW / 4; ++e) {
+        o[2 * e] = fma_f32x2(y[e].x, f2, o[2 * e]);
+        o[2 * e + 1] = fma_f32x2(y[e].y, f2, o[2 * e + 1]);
+      }
+    }
+    const float total = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const uint64_t t2 = pair_f32(total, total);
+#pragma unroll
+    for (int e = 0; e < kW / 2; ++e) o[e] = fma_f32x2(o[e], t2, 0ull);
+    pack_all();
+    store(w, c);
+    if (c == 0) store_lse();
+  }
+}
+
 template <int kD, int kSrc>
 __global__ void __launch_bounds__(kRwThreads, 1)
     rows_tc_kernel(const RowsParams p, const __grid_constant__ CUtensorMap tmap_q,
@@ -244,7 +357,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     }
     for (int i = 0; i < kRwItems; ++i) {
       mbar_init(&S.ifull[i], 1);
-      mbar_init(&S.iempty[i], 8 + 4 + 1);  // softmax and epilogue warps, the issuer
+      mbar_init(&S.iempty[i], 8 + 1);  // softmax warps, the issuer
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.qfull[i], 1);
@@ -253,12 +366,9 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       mbar_init(&S.pfull[i][0], 4);
       mbar_init(&S.pfull[i][1], 4);
       mbar_init(&S.ofin[i], 1);
-      mbar_init(&S.oempty[i], 4);
-      for (int j = 0; j < 2; ++j) {
-        mbar_init(&S.lready[i][j], 4);
-        mbar_init(&S.lfree[i][j], 4);
-      }
+      mbar_init(&S.oempty[i], 8);
     }
+    for (int q = 0; q < 4; ++q) mbar_init(&S.xpair[q], 2);
     mbar_init(&S.drain, 1);
     S.abort_flag = 0;
     S.bad = 0;
@@ -321,7 +431,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
   const uint32_t tmem = S.tmem_base;
 
   if (warp >= kRwProducer) {
-    set_regs_less<72>();
+    set_regs_less<88>();
     if (warp == kRwProducer) {
       // ======================= plan and TMA =======================
       // Totals of the threads' stretches, 16 a lane, then this CTA's stretch of the work.
@@ -557,9 +667,11 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           if (!row_wait_warp(&S.pfull[L][half], (st.J - 1) & 1u, &S.abort_flag)) return false;
           tc_fence_after();
           if (elect_one()) {
-#pragma unroll 1
-            for (uint32_t kk = 4 * half; kk < min(st.steps, 4 * half + 4); ++kk)
-              umma_bf16_ts(o_col, s_col + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, kk > 0 ? 1u : acc);
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+              const uint32_t kk = 4 * half + i;
+              if (kk < st.steps) umma_bf16_ts(o_col, s_col + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, kk > 0 ? 1u : acc);
+            }
           }
           __syncwarp();
         }
@@ -632,67 +744,51 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         begin(1, st1);
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.iempty[slot]);
-        // Tiles [2, plain) of a two-tile item: both lanes use them, neither the product of the tile before
-        // nor the scores are an item's first or last. The general turns below cost the issuing warp
-        // ~600 cycles of bookkeeping each, which left the tensor pipe idle as long.
-        const int plain = st0.step == 1 ? st0.used - 1 : 0;
+        // Tiles [1, used) of a two-tile item, which both lanes use: the products of the tile before are
+        // whole. The general turns below cost the issuing warp ~600 cycles of bookkeeping each, which
+        // leaves the tensor pipe idle as long.
+        const int plain = st0.step == 1 ? st0.used : 0;
         for (int j = 0; ok && j < ntile; ++j, ++T) {
-          if (j == 2 && plain > 2) {
+          if (j == 1 && plain > 1) {
             uint32_t sk = 2 * T % kStages, pk = (2 * T / kStages) & 1u;          // K of tile T
             uint32_t sv = (2 * T - 1) % kStages, pv = ((2 * T - 1) / kStages) & 1u;  // V of tile T - 1
             uint32_t p0 = (st0.J - 1) & 1u, p1 = (st1.J - 1) & 1u;
-            const int n = plain - 2;
+            const uint32_t po = (K & 1u) ^ 1u;
+            auto lane_turn = [&](auto lane_no, uint32_t parity, uint32_t acc, uint64_t kd, uint64_t vd, bool last) -> bool {
+              constexpr int L = decltype(lane_no)::value;
+              if (!row_wait_warp(&S.pfull[L][0], parity, &S.abort_flag)) return false;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_bf16_ts(tm + kRwColO + kD * L, tm + 128 * L + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, kk > 0 ? 1u : acc);
+              }
+              if (!row_wait_warp(&S.pfull[L][1], parity, &S.abort_flag)) return false;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 4; kk < 8; ++kk)
+                  umma_bf16_ts(tm + kRwColO + kD * L, tm + 128 * L + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
+                umma_commit(&S.empty[sv]);
+#pragma unroll
+                for (int kk = 0; kk < kD / 16; ++kk) {
+                  const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kRwHalf >> 4) + (kk & 3) * 2);
+                  umma_bf16_ss(tm + 128 * L, q_desc + L * kStageDesc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&S.sfull[L]);
+                if (last) umma_commit(&S.qempty[L]);
+              }
+              __syncwarp();
+              return true;
+            };
+            const int n = plain - 1;
             for (int i = 0; i < n; ++i) {
               const uint64_t kd = k_desc + static_cast<uint64_t>(sk * kStageDesc), vd = v_desc + static_cast<uint64_t>(sv * kStageDesc);
-              ok = row_wait_warp(&S.full[sv], pv, &S.abort_flag) && row_wait_warp(&S.full[sk], pk, &S.abort_flag) &&
-                   row_wait_warp(&S.pfull[0][0], p0, &S.abort_flag);
+              ok = row_wait_warp(&S.full[sv], pv, &S.abort_flag) && row_wait_warp(&S.full[sk], pk, &S.abort_flag);
+              if (i == 0) ok = ok && row_wait_warp(&S.oempty[0], po, &S.abort_flag) && row_wait_warp(&S.oempty[1], po, &S.abort_flag);
+              const uint32_t acc = i > 0 ? 1u : 0u;
+              ok = ok && lane_turn(lane0, p0, acc, kd, vd, i == n - 1) && lane_turn(lane1, p1, acc, kd, vd, i == n - 1 && st1.used == plain);
               if (!ok) break;
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  umma_bf16_ts(tm + kRwColO, tm + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
-              }
-              ok = row_wait_warp(&S.pfull[0][1], p0, &S.abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int kk = 4; kk < 8; ++kk)
-                  umma_bf16_ts(tm + kRwColO, tm + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
-#pragma unroll
-                for (int kk = 0; kk < kD / 16; ++kk) {
-                  const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kRwHalf >> 4) + (kk & 3) * 2);
-                  umma_bf16_ss(tm, q_desc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-                }
-                umma_commit(&S.sfull[0]);
-              }
-              __syncwarp();
-              ok = row_wait_warp(&S.pfull[1][0], p1, &S.abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  umma_bf16_ts(tm + kRwColO + kD, tm + 128 + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
-              }
-              ok = row_wait_warp(&S.pfull[1][1], p1, &S.abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int kk = 4; kk < 8; ++kk)
-                  umma_bf16_ts(tm + kRwColO + kD, tm + 128 + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
-                umma_commit(&S.empty[sv]);
-                umma_commit(&S.empty[sv]);
-#pragma unroll
-                for (int kk = 0; kk < kD / 16; ++kk) {
-                  const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kRwHalf >> 4) + (kk & 3) * 2);
-                  umma_bf16_ss(tm + 128, q_desc + kStageDesc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
-                }
-                umma_commit(&S.sfull[1]);
-              }
-              __syncwarp();
               if ((sk += 2) >= kStages) { sk -= kStages; pk ^= 1u; }
               if ((sv += 2) >= kStages) { sv -= kStages; pv ^= 1u; }
               p0 ^= 1u;
@@ -703,15 +799,17 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             T += n;
             auto forward = [&](Turn& st) {
               st.pend = T;
-              st.steps = 8;
-              st.first = st.last = 0;
+              st.steps = static_cast<uint32_t>(min(128, st.kend - (j - 1) * 128) + 15) >> 4;
+              st.first = 0;
               st.alone = false;
               st.i += n;
+              st.last = st.i == st.used;
               st.next += n;
               st.J += n;
             };
             forward(st0);
             forward(st1);
+            if (j >= ntile) break;
           }
           const bool use0 = st0.i < st0.used && j == st0.next, use1 = st1.i < st1.used && j == st1.next;
           ok = turn(lane0, st0, K, j, use0, use1) && turn(lane1, st1, K, j, use1, use0);
@@ -725,13 +823,13 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       (void)row_poll(&S.drain, 0);
     }
     __syncwarp();
-  } else if (warp < kRwEpi) {
-    // ======================= softmax of one lane, one row a thread =======================
-    set_regs_more<176>();
+  } else {
+    // ======================= softmax and output of one lane, one row a thread =======================
+    set_regs_more<208>();
     const int L = warp >> 2, quad = warp & 3;
     const int r = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t s_col = tmem + lane_base + 128 * L, o_col = tmem + lane_base + kRwColO + kD * L;
+    const uint32_t o_base = tmem + lane_base + kRwColO, s_col = tmem + lane_base + 128 * L, o_col = o_base + kD * L;
     const int pos_in = (r * p.g_recip16) >> 16;  // r / G
     const uint64_t scale2 = pair_f32(p.scale_log2, p.scale_log2);
     uint32_t T = 0, J = 0;
@@ -761,44 +859,20 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         tc_fence_after();
         // K of this tile is no longer read (its stage expects two arrivals; a tile of one lane gives both)
         if (warp == 4 * L && lane == 0) mbar_arrive_n(&S.empty[2 * (T + j) % kStages], i < both ? 1u : 2u);
-        uint32_t x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
-        tmem_wait_ld();
         if (!full) {
-#pragma unroll
-          for (int e = 0; e < 128; ++e) x[e] = (w[e >> 5] >> (e & 31)) & 1u ? x[e] : 0xff800000u;
-        }
-        float mx[4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a) mx[a] = max3_f32(__uint_as_float(x[2 * a]), __uint_as_float(x[2 * a + 1]), -INFINITY);
-#pragma unroll
-        for (int e = 8; e < 128; e += 8)
-#pragma unroll
-          for (int a = 0; a < 4; ++a)
-            mx[a] = max3_f32(mx[a], __uint_as_float(x[e + 2 * a]), __uint_as_float(x[e + 2 * a + 1]));
-        const float mn = max3_f32(m, max3_f32(max3_f32(mx[0], mx[1], mx[2]), mx[3], -INFINITY) * p.scale_log2, -INFINITY);
-        const bool move = !(mn <= m + kRwRescale);  // from -inf, and for NaN too
-        if (i > 0 && __any_sync(0xffffffffu, move)) {
-          // the scores of this tile were issued after the last product into O had completed
-          const float alpha = move ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
+          // in tensor memory, so that the scores below come straight from there in every tile
 #pragma unroll 1
-          for (int c = 0; c < kD; c += 16) {
-            uint32_t o[16];
-            tmem_ld16(o_col + c, o);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[32];
+            tmem_ld32(s_col + 32 * c, y);
             tmem_wait_ld();
+            const uint32_t bits = c < 2 ? (c == 0 ? w[0] : w[1]) : (c == 2 ? w[2] : w[3]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(o_col + c, o);
+            for (int e = 0; e < 32; ++e) y[e] = (bits >> e) & 1u ? y[e] : 0xff800000u;
+            tmem_st32(s_col + 32 * c, y);
           }
-          const uint64_t alpha2 = pair_f32(alpha, alpha);
-#pragma unroll
-          for (int a = 0; a < 4; ++a) sum2[a] = fma_f32x2(sum2[a], alpha2, 0ull);
+          tmem_wait_st();
         }
-        if (move) m = mn;
-        // -m; 0 where every score is -inf so far, NaN for a row that saw +inf (as for one that saw NaN)
-        const float negm = m == -INFINITY ? 0.f : fmaf(m, 0.f, -m);
-        const uint64_t negm2 = pair_f32(negm, negm);
         const int valid = it.k1 - tile * 128;
         if (valid < 128 && (valid & 15) != 0) {
           // zero V rows [valid, next multiple of 16): they may lie behind the request's keys
@@ -812,33 +886,82 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        // P in two halves of 64 keys, so that the product with V starts before the second is done; a
-        // half is reported one 32-key step late, when its stores have long landed
+        uint32_t x[128];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
+        tmem_wait_ld();
+        // P of keys 32 c + [0, 32), from the maximum m; their sums into add2
+        uint64_t add2[4];
+        auto weights = [&](int c, uint64_t negm2) {
           uint32_t out[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             const uint64_t a = fma_f32x2(pair_f32(__uint_as_float(x[32 * c + e]), __uint_as_float(x[32 * c + e + 1])), scale2, negm2);
             float a0, a1;
-            if ((e >> 1) % kRwPolyEvery == kRwPolyEvery - 1) {
-              exp2_poly(a, a0, a1);
-            } else {
-              unpair_f32(a, a0, a1);
-              a0 = fast_exp2(a0);
-              a1 = fast_exp2(a1);
-            }
+            unpair_f32(a, a0, a1);
+            a0 = fast_exp2(a0);
+            a1 = fast_exp2(a1);
             out[e >> 1] = pack_bf16(a0, a1);
-            sum2[(e >> 1) & 3] = add_f32x2(sum2[(e >> 1) & 3], pair_f32(a0, a1));
-          }
-          if (c == 2) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.pfull[L][0]);
+            add2[(e >> 1) & 3] = add_f32x2(add2[(e >> 1) & 3], pair_f32(a0, a1));
           }
           tmem_st16(s_col + 16 * c, out);
+        };
+        // -m; 0 where every score is -inf so far, NaN for a row that saw +inf (as for one that saw NaN)
+        auto minus = [&]() {
+          const float n = m == -INFINITY ? 0.f : fmaf(m, 0.f, -m);
+          return pair_f32(n, n);
+        };
+        // The first half of the tile is weighted with the maximum so far while the whole tile's maximum
+        // is found beside it; only where that has grown by more than 2^8 is it weighted again.
+        bool checked = false;
+        for (;;) {
+#pragma unroll
+          for (int a = 0; a < 4; ++a) add2[a] = 0;
+          if (i > 0 || checked) {
+            const uint64_t negm2 = minus();
+            weights(0, negm2);
+            weights(1, negm2);
+          }
+          if (checked) break;
+          checked = true;
+          float mx[4];
+#pragma unroll
+          for (int a = 0; a < 4; ++a) mx[a] = max3_f32(__uint_as_float(x[2 * a]), __uint_as_float(x[2 * a + 1]), -INFINITY);
+#pragma unroll
+          for (int e = 8; e < 128; e += 8)
+#pragma unroll
+            for (int a = 0; a < 4; ++a)
+              mx[a] = max3_f32(mx[a], __uint_as_float(x[e + 2 * a]), __uint_as_float(x[e + 2 * a + 1]));
+          const float mn = max3_f32(m, max3_f32(max3_f32(mx[0], mx[1], mx[2]), mx[3], -INFINITY) * p.scale_log2, -INFINITY);
+          const bool move = !(mn <= m + kRwRescale);  // from -inf, and for NaN too
+          if (i > 0 && !__any_sync(0xffffffffu, move)) break;
+          const float alpha = move ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
+          if (move) m = mn;
+          if (i > 0) {
+            // the scores of this tile were issued after the last product into O had completed
+#pragma unroll 1
+            for (int c = 0; c < kD; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_col + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st16(o_col + c, o);
+            }
+            const uint64_t alpha2 = pair_f32(alpha, alpha);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) sum2[a] = fma_f32x2(sum2[a], alpha2, 0ull);
+          }
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.pfull[L][0]);
+        const uint64_t negm2 = minus();
+        weights(2, negm2);
+        weights(3, negm2);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) sum2[a] = add_f32x2(sum2[a], add2[a]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -846,211 +969,38 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       }
       if (!ok) break;
       T += it.ntile;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.iempty[slot]);
-      float s[8];
+      float l, f0 = 1.f, f1 = 0.f;  // O = f0 O_lane0 + f1 O_lane1 (alt)
+      {
+        float s[8];
 #pragma unroll
-      for (int a = 0; a < 4; ++a) unpair_f32(sum2[a], s[2 * a], s[2 * a + 1]);
-      const uint32_t ob = K & 1;
-      if (!row_wait(&S.lfree[ob][L], ((K >> 1) & 1u) ^ 1u, &S.abort_flag)) break;
-      S.mfin[ob][L][r] = m;
-      // a row that saw no key has only the polynomial's 2^-126 in its sums
-      S.lfin[ob][L][r] = m == -INFINITY ? 0.f : ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.lready[ob][L]);
-    }
-  } else {
-    // ======================= epilogue: outputs, or the pieces of cut items =======================
-    set_regs_less<88>();
-    const int quad = warp & 3, r = quad * 32 + lane;
-    const uint32_t o_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + kRwColO;
-    const int pos_in = (r * p.g_recip16) >> 16, head_in = r - pos_in * p.g;
-    // pieces: O as [slot][lane][D / 4][128 rows] float4, (m, l) as [slot][lane][128] float2
-    float4* part_o = reinterpret_cast<float4*>(p.part_o);
-    float2* part_ml = reinterpret_cast<float2*>(p.part_ml);
-    bool ok = true;
-    for (uint32_t K = 0; ok; ++K) {
-      const int slot = K & (kRwItems - 1);
-      if (!row_wait(&S.ifull[slot], (K / kRwItems) & 1u, &S.abort_flag)) break;
-      const RowItem& it = S.item[slot];
-      if (it.stop) break;
-      const uint32_t ob = K & 1;
-      const int tiles = it.alt ? 1 : 2;  // row tiles
-      // 32 columns of a row as 16 bf16 pairs, a row's 16 x kD / 32 pairs to memory, its log-sum-exp
-      auto pack = [&](const float (&o)[32], float inv, uint32_t* to) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) to[e] = pack_bf16(o[2 * e] * inv, o[2 * e + 1] * inv);
-      };
-      auto store_lse = [&](int t, float m, float l) {
-        p.lse[(static_cast<int64_t>(it.row0) + pos_in + t * tpt) * p.hq + it.h * p.g + head_in] =
-            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      };
-      auto out_row = [&](int t) {
-        return reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
-                                        (static_cast<int64_t>(it.row0) + pos_in + t * tpt) * p.o_sr +
-                                        static_cast<int64_t>(it.h * p.g + head_in) * p.o_sh);
-      };
-      for (int t = 0; t < tiles; ++t) {
-        const bool row_ok = pos_in < it.tokens[t];
-        float m, l, f0 = 1.f, f1 = 0.f;  // O = f0 O_first + f1 O_second
-        for (int L = t; L < (it.alt ? 2 : t + 1); ++L) {
-          if (!row_wait(&S.lready[ob][L], (K >> 1) & 1u, &S.abort_flag)) { ok = false; break; }
-          const float ml = S.mfin[ob][L][r], ll = S.lfin[ob][L][r];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.lfree[ob][L]);
-          if (L == t) {
-            m = ml;
-            l = ll;
-          } else {  // the other lane's key tiles of the same rows
-            const float mn = fmaxf(m, ml);
-            f0 = l > 0.f ? fast_exp2(m - mn) : 0.f;
-            f1 = ll > 0.f ? fast_exp2(ml - mn) : 0.f;
-            l = l * f0 + ll * f1;
-            m = mn;
-          }
-          if (!row_wait(&S.ofin[L], K & 1u, &S.abort_flag)) { ok = false; break; }
-        }
-        if (!ok) break;
-        tc_fence_after();
-        // Columns c .. c + 31 of the row, times `scale`. A lane without tiles has left its accumulator
-        // as it was: that one is not looked at.
-        const bool none0 = it.used[t] == 0, none1 = it.used[1] == 0;
-        auto read = [&](int c, float scale, uint64_t (&o)[16]) {
-          uint32_t raw[32];
-          tmem_ld32(o_base + kD * t + c, raw);
-          tmem_wait_ld();
-          const float s0 = scale * f0, s1 = scale * f1;
-          const uint64_t s02 = pair_f32(s0, s0), s12 = pair_f32(s1, s1);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            o[e] = none0 ? 0ull : fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s02, 0ull);
-          if (it.alt && !none1) {
-            tmem_ld32(o_base + kD + c, raw);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              o[e] = fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s12, o[e]);
-          }
-        };
-        if (it.cuts == 0) {
-          // 64 columns at a time through shared memory, so that eight lanes store a row's 128 bytes:
-          // a thread storing its own row kept the load/store pipe, and with it every warp's barrier
-          // and tensor-memory traffic, busy for ~3000 cycles an item.
-          const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll 1
-          for (int c0 = 0; c0 < kD; c0 += 64) {
-#pragma unroll 1
-            for (int c = 0; c < 64; c += 32) {
-              uint64_t o[16];
-              uint32_t w[16];
-              read(c0 + c, inv, o);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float lo, hi;
-                unpair_f32(o[e], lo, hi);
-                w[e] = pack_bf16(lo, hi);
-              }
-              uint4* dst = reinterpret_cast<uint4*>(S.stage[quad][lane] + c * 2);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-            }
-            if (c0 + 64 == kD) {  // the accumulator is read: the next item's first product may start
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) {
-                mbar_arrive(&S.oempty[t]);
-                if (it.alt) mbar_arrive(&S.oempty[1]);
-              }
-            }
-            __syncwarp();
-#pragma unroll 2
-            for (int i = 0; i < 32; i += 4) {
-              const int row = i + (lane >> 3), rr = quad * 32 + row;
-              const int rpos = (rr * p.g_recip16) >> 16;
-              const uint4 x = *reinterpret_cast<const uint4*>(S.stage[quad][row] + (lane & 7) * 16);
-              if (rpos < it.tokens[t])
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
-                                          (static_cast<int64_t>(it.row0) + rpos + t * tpt) * p.o_sr +
-                                          static_cast<int64_t>(it.h * p.g + rr - rpos * p.g) * p.o_sh + c0 + (lane & 7) * 8) = x;
-            }
-            __syncwarp();
-          }
-          if (row_ok) store_lse(t, m, l);
-        } else {
-          const int part = 2 * static_cast<int>(blockIdx.x) + (it.piece > 0 ? 0 : 1);
-#pragma unroll 1
-          for (int c = 0; c < kD; c += 32) {
-            uint64_t o[16];
-            read(c, 1.f, o);
-            ulonglong2* dst = reinterpret_cast<ulonglong2*>(part_o) + ((static_cast<int64_t>(part) * 2 + t) * (kD / 4) + c / 4) * 128 + r;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e * 128] = make_ulonglong2(o[2 * e], o[2 * e + 1]);
-          }
-          part_ml[(static_cast<int64_t>(part) * 2 + t) * 128 + r] = make_float2(m, l);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&S.oempty[t]);
-            if (it.alt) mbar_arrive(&S.oempty[1]);
-          }
-        }
+        for (int a = 0; a < 4; ++a) unpair_f32(sum2[a], s[2 * a], s[2 * a + 1]);
+        l = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
       }
-      if (!ok) break;
-      if (it.cuts > 0) {
-        // The quad's rows of this piece are written; the warp that counts the last piece adds them all.
-        __threadfence();
+      if (!row_wait(&S.ofin[L], K & 1u, &S.abort_flag)) break;
+      if (alt) {
+        // the other lane's part of the row: post, meet, read, and meet again before anyone posts again
+        S.xend[warp][lane] = make_float2(m, l);
         __syncwarp();
-        uint32_t before = 0;
-        uint32_t* counter = &p.hdr->row_pieces[it.cut0];
-        if (lane == 0) before = (atomicAdd(counter, 1u << (8 * quad)) >> (8 * quad)) & 0xffu;
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before == static_cast<uint32_t>(it.cuts)) {
-          __threadfence();
-          if (lane == 0) atomicSub(counter, static_cast<uint32_t>(it.cuts + 1) << (8 * quad));
-          auto piece_slot = [&](int q) { return 2 * (it.cut0 - 1 + q) + (q > 0 ? 0 : 1); };
-          for (int t = 0; t < tiles; ++t) {
-            const bool row_ok = pos_in < it.tokens[t];
-            float m = -INFINITY, l = 0.f;
-            for (int q = 0; q <= it.cuts; ++q) {
-              const float2 ml = __ldcg(part_ml + (static_cast<int64_t>(piece_slot(q)) * 2 + t) * 128 + r);
-              if (!(ml.y == 0.f)) m = fmaxf(m, ml.x);
-            }
-            for (int q = 0; q <= it.cuts; ++q) {
-              const float2 ml = __ldcg(part_ml + (static_cast<int64_t>(piece_slot(q)) * 2 + t) * 128 + r);
-              if (!(ml.y == 0.f)) l = fmaf(ml.y, fast_exp2(ml.x - m), l);
-            }
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        if (lane == 0) mbar_arrive(&S.xpair[quad]);
+        if (!row_wait(&S.xpair[quad], 0u, &S.abort_flag)) break;
+        const float2 y = S.xend[warp ^ 4][lane];
+        const float ma = L == 0 ? m : y.x, mb = L == 0 ? y.x : m, la = L == 0 ? l : y.y, lb = L == 0 ? y.y : l;
+        m = fmaxf(ma, mb);
+        f0 = la == 0.f ? 0.f : fast_exp2(ma - m);
+        f1 = lb == 0.f ? 0.f : fast_exp2(mb - m);
+        l = la * f0 + lb * f1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.xpair[quad]);
+        if (!row_wait(&S.xpair[quad], 1u, &S.abort_flag)) break;
+        if (!row_wait(&S.ofin[L ^ 1], K & 1u, &S.abort_flag)) break;
+      }
+      tc_fence_after();
+      if (alt) {
+        row_output<kD, kD / 2, true>(p, S, it, warp, lane, 0, L * (kD / 2), true, o_base, tpt, m, l, f0, f1);
+      } else {
 #pragma unroll 1
-            for (int c = 0; c < kD; c += 32) {
-              float o[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.f;
-#pragma unroll 1
-              for (int q = 0; q <= it.cuts; ++q) {
-                const int64_t at = static_cast<int64_t>(piece_slot(q)) * 2 + t;
-                const float2 ml = __ldcg(part_ml + at * 128 + r);
-                const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);
-                const float4* src = part_o + (at * (kD / 4) + c / 4) * 128 + r;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float4 y = __ldcg(src + e * 128);
-                  o[4 * e] = fmaf(f, y.x, o[4 * e]);
-                  o[4 * e + 1] = fmaf(f, y.y, o[4 * e + 1]);
-                  o[4 * e + 2] = fmaf(f, y.z, o[4 * e + 2]);
-                  o[4 * e + 3] = fmaf(f, y.w, o[4 * e + 3]);
-                }
-              }
-              if (row_ok) {
-                uint32_t w[16];
-                pack(o, inv, w);
-                uint4* dst = out_row(t) + c / 8;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-              }
-            }
-            if (row_ok) store_lse(t, m, l);
-          }
-        }
+        for (int c = 0; c < kD; c += 64)
+          row_output<kD, 64, false>(p, S, it, warp, lane, L, c, c + 64 == kD, o_base + kD * L, tpt, m, l, 1.f, 0.f);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.iempty[slot]);
@@ -1087,7 +1037,7 @@ cudaError_t launch_rows_t(const RowsParams& p, const CUtensorMap& tq, const CUte
 }  // namespace
 
 size_t rows_workspace_bytes(int d, int nctas) {
-  return sizeof(WsHeader) + static_cast<size_t>(2 * nctas) * 2 * 128 * (d * sizeof(float) + sizeof(float2));
+  return sizeof(WsHeader) + static_cast<size_t>(2 * nctas) * (2 * 128 * d * sizeof(float) + 8 * 32 * sizeof(float2));
 }
 
 cudaError_t launch_rows(RowsParams p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int nctas,
