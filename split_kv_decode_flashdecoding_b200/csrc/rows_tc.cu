@@ -77,7 +77,7 @@ struct __align__(1024) RwSmem {
       int64_t part_w[kRwThreads];
       int32_t part_r[kRwThreads], part_i[kRwThreads];
     };
-    uint4 stage[8][64];  // output: eight rows of 64 columns of a warp
+    uint4 stage[8][128];  // output: a warp's rows, 32 columns
   };
   uint64_t full[kStages], empty[kStages];
   uint64_t qfull[2], qempty[2], ifull[kRwItems], iempty[kRwItems];
@@ -198,99 +198,100 @@ __device__ __forceinline__ void visible_words(const RowsParams& p, const RowItem
   }
 }
 
-// The end of an item for one softmax warp: columns c0 + [0, kW) of its 32 rows of row tile t (`last`:
-// its last ones), the accumulator(s) at o_base (an alt item: both lanes', times f0 and f1) over l, to memory; or, for a
-// piece of a cut item, unscaled to the workspace, where the warp that counts the last piece adds
-// them all in piece order. Rows leave through shared memory, eight at a time, so that neighbouring
-// threads store neighbouring bytes: a thread storing its own row kept the load/store pipe, and with
-// it every warp's barrier and tensor-memory traffic, busy for ~3000 cycles an item.
-template <int kD, int kW, bool kAlt, typename Smem>
+// The end of an item for one softmax warp: columns [c0, c1) of its 32 rows of row tile t, the
+// accumulator at o_col (an alt item: both lanes', times f0 and f1) over l, to memory; or, for a piece of
+// a cut item, unscaled to the workspace, where the warp that counts the last piece adds them all in
+// piece order. Rows leave through shared memory, 32 columns at a time, so that neighbouring threads
+// store neighbouring bytes: a thread storing its own row kept the load/store pipe, and with it every
+// warp's barrier and tensor-memory traffic, busy for ~3000 cycles an item. The loops stay rolled: this
+// code runs once an item, from a cold instruction cache.
+template <int kD, bool kAlt, typename Smem>
 __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const RowItem& it, int warp, int lane, int t,
-                                           int c0, bool last, uint32_t o_base, int tpt, float m, float l, float f0, float f1) {
-  constexpr int kUnits = kW / 8;  // 16-byte units of a row's columns
+                                           int c0, int c1, uint32_t o_col, int tpt, float m, float l, float f0, float f1) {
   const int quad = warp & 3;
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  auto store = [&](const uint32_t (&w)[kW / 2], int c) {
-    uint4* stage = S.stage[warp];
-#pragma unroll 1
-    for (int g = 0; g < 4; ++g) {
-      __syncwarp();
-      if ((lane >> 3) == g) {
+  uint4* stage = S.stage[warp];
+  // this thread's stores: 16 bytes of rows lane / 4 + 8 i
+  char* dst[4];
 #pragma unroll
-        for (int e = 0; e < kUnits; ++e)
-          stage[(lane & 7) * kUnits + (e ^ (lane & (kUnits - 1)))] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-      }
-      __syncwarp();
-#pragma unroll
-      for (int n = lane; n < 8 * kUnits; n += 32) {
-        const int row = n / kUnits, e = n % kUnits;
-        const int rr = quad * 32 + g * 8 + row, pos = (rr * p.g_recip16) >> 16;
-        const uint4 v = stage[row * kUnits + (e ^ (row & (kUnits - 1)))];
-        if (pos < it.tokens[t])
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
-                                    (static_cast<int64_t>(it.row0) + pos + t * tpt) * p.o_sr +
-                                    static_cast<int64_t>(it.h * p.g + rr - pos * p.g) * p.o_sh + c + e * 8) = v;
-      }
-    }
-  };
-  auto store_lse = [&]() {
-    const int r = quad * 32 + lane, pos = (r * p.g_recip16) >> 16;
-    if (pos < it.tokens[t])
-      p.lse[(static_cast<int64_t>(it.row0) + pos + t * tpt) * p.hq + it.h * p.g + r - pos * p.g] =
-          l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-  };
-  // A lane without tiles has left its accumulator as it was: that one is not looked at.
-  const bool none0 = it.used[kAlt ? 0 : t] == 0, none1 = it.used[1] == 0;
-  const float scale = it.cuts == 0 ? inv : 1.f;
-  const float s0 = scale * f0, s1 = scale * f1;
-  const uint64_t s02 = pair_f32(s0, s0), s12 = pair_f32(s1, s1);
-  uint64_t o[kW / 2];
-#pragma unroll
-  for (int c = 0; c < kW; c += 16) {
-    uint32_t raw[16];
-    tmem_ld16(o_base + c0 + c, raw);
-    tmem_wait_ld();
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      o[c / 2 + e] = none0 ? 0ull : fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s02, 0ull);
-    if (kAlt && !none1) {
-      tmem_ld16(o_base + kD + c0 + c, raw);
-      tmem_wait_ld();
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        o[c / 2 + e] = fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s12, o[c / 2 + e]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int rr = quad * 32 + (lane >> 2) + 8 * i, pos = (rr * p.g_recip16) >> 16;
+    dst[i] = pos < it.tokens[t] ? static_cast<char*>(p.out) + 2 * ((static_cast<int64_t>(it.row0) + pos + t * tpt) * p.o_sr +
+                                                                   static_cast<int64_t>(it.h * p.g + rr - pos * p.g) * p.o_sh) +
+                                      16 * (lane & 3)
+                                : nullptr;
   }
-  tc_fence_before();
-  __syncwarp();
-  if (last && lane == 0) {  // the accumulator is read: the next item's first product may start
-    mbar_arrive_n(&S.oempty[t], kAlt ? 1u : 2u);
-    if (kAlt) mbar_arrive_n(&S.oempty[1], 1u);
-  }
-  uint32_t w[kW / 2];
-  auto pack_all = [&]() {
+  auto emit = [&](int c, const uint64_t (&o)[16]) {
+    uint32_t w[16];
 #pragma unroll
-    for (int e = 0; e < kW / 2; ++e) {
+    for (int e = 0; e < 16; ++e) {
       float lo, hi;
       unpair_f32(o[e], lo, hi);
       w[e] = pack_bf16(lo, hi);
     }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) stage[lane * 4 + (e ^ ((lane >> 1) & 3))] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = (lane >> 2) + 8 * i;
+      const uint4 v = stage[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
+      if (dst[i]) *reinterpret_cast<uint4*>(dst[i] + 2 * c) = v;
+    }
   };
-  if (it.cuts == 0) {
-    pack_all();
-    store(w, c0);
-    if (c0 == 0) store_lse();
+  auto store_lse = [&](float m, float l) {
+    const int r = quad * 32 + lane, pos = (r * p.g_recip16) >> 16;
+    if (c0 == 0 && pos < it.tokens[t])
+      p.lse[(static_cast<int64_t>(it.row0) + pos + t * tpt) * p.hq + it.h * p.g + r - pos * p.g] =
+          l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  };
+  auto over = [](float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); };  // 0 for an empty row; NaN stays
+  // pieces: O as [slot][row tile][D / 4][128 rows] float4, (m, l) as [slot][warp][32 rows] float2
+  ulonglong2* part_o = reinterpret_cast<ulonglong2*>(p.part_o) + quad * 32 + lane;
+  float2* part_ml = reinterpret_cast<float2*>(p.part_ml) + warp * 32 + lane;
+  auto place = [&](int64_t slot, int c) { return ((slot * 2 + t) * (kD / 4) + c / 4) * 128; };
+  const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (it.piece > 0 ? 0 : 1);
+  const bool whole = it.cuts == 0;
+  // A lane without tiles has left its accumulator as it was: that one is not looked at.
+  const bool none0 = it.used[kAlt ? 0 : t] == 0, none1 = it.used[1] == 0;
+  const float scale = whole ? over(l) : 1.f;
+  const uint64_t s02 = pair_f32(scale * f0, scale * f0), s12 = pair_f32(scale * f1, scale * f1);
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 32) {
+    uint64_t o[16];
+    uint32_t raw[32];
+    tmem_ld32(o_col + c, raw);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      o[e] = none0 ? 0ull : fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s02, 0ull);
+    if (kAlt && !none1) {
+      tmem_ld32(o_col + kD + c, raw);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        o[e] = fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s12, o[e]);
+    }
+    if (c + 32 >= c1) {  // the accumulator is read: the next item's first product may start
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive_n(&S.oempty[t], kAlt ? 1u : 2u);
+        if (kAlt) mbar_arrive_n(&S.oempty[1], 1u);
+      }
+    }
+    if (whole) {
+      emit(c, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part_o[place(part, c) + e * 128] = make_ulonglong2(o[2 * e], o[2 * e + 1]);
+    }
+  }
+  if (whole) {
+    store_lse(m, l);
     return;
   }
-  // pieces: O as [slot][row tile][D / 4][128 rows] float4, (m, l) as [slot][warp][32 rows] float2
-  ulonglong2* part_o = reinterpret_cast<ulonglong2*>(p.part_o);
-  float2* part_ml = reinterpret_cast<float2*>(p.part_ml);
-  const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (it.piece > 0 ? 0 : 1);
-  auto place = [&](int64_t slot, int c) { return ((slot * 2 + t) * (kD / 4) + c / 4) * 128 + quad * 32 + lane; };
-#pragma unroll
-  for (int e = 0; e < kW / 4; ++e) part_o[place(part, c0) + e * 128] = make_ulonglong2(o[2 * e], o[2 * e + 1]);
-  part_ml[(part * 8 + warp) * 32 + lane] = make_float2(m, l);
-  if (!last) return;
+  part_ml[part * 256] = make_float2(m, l);
   __threadfence();
   __syncwarp();
   uint32_t* counter = &p.hdr->row_pieces[it.cut0][warp >> 2];
@@ -301,40 +302,38 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
   __threadfence();
   if (lane == 0) atomicSub(counter, static_cast<uint32_t>(it.cuts + 1) << (8 * quad));
   auto piece_slot = [&](int q) { return 2 * static_cast<int64_t>(it.cut0 - 1 + q) + (q > 0 ? 0 : 1); };
-  m = -INFINITY;
+  float mt = -INFINITY, lt = 0.f;
   for (int q = 0; q <= it.cuts; ++q) {
-    const float2 ml = __ldcg(part_ml + (piece_slot(q) * 8 + warp) * 32 + lane);
-    if (!(ml.y == 0.f)) m = fmaxf(m, ml.x);
+    const float2 ml = __ldcg(part_ml + piece_slot(q) * 256);
+    if (!(ml.y == 0.f)) mt = fmaxf(mt, ml.x);
   }
+  for (int q = 0; q <= it.cuts; ++q) {
+    const float2 ml = __ldcg(part_ml + piece_slot(q) * 256);
+    if (!(ml.y == 0.f)) lt = fmaf(ml.y, fast_exp2(ml.x - mt), lt);
+  }
+  const float total = over(lt);
 #pragma unroll 1
-  for (int c = kAlt ? c0 : 0; c <= c0; c += kW) {
-    l = 0.f;
+  for (int c = c0; c < c1; c += 32) {
+    uint64_t o[16];
 #pragma unroll
-    for (int e = 0; e < kW / 2; ++e) o[e] = 0;
-#pragma unroll 1
+    for (int e = 0; e < 16; ++e) o[e] = 0;
+#pragma unroll 2
     for (int q = 0; q <= it.cuts; ++q) {
-      const ulonglong2* src = part_o + place(piece_slot(q), c);
-      ulonglong2 y[kW / 4];
+      const float2 ml = __ldcg(part_ml + piece_slot(q) * 256);
+      ulonglong2 y[8];
 #pragma unroll
-      for (int e = 0; e < kW / 4; ++e) y[e] = __ldcg(src + e * 128);
-      const float2 ml = __ldcg(part_ml + (piece_slot(q) * 8 + warp) * 32 + lane);
-      const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - m);
-      l = fmaf(ml.y, f, l);
+      for (int e = 0; e < 8; ++e) y[e] = __ldcg(part_o + place(piece_slot(q), c) + e * 128);
+      const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - mt) * total;
       const uint64_t f2 = pair_f32(f, f);
 #pragma unroll
-      for (int e = 0; e < kW / 4; ++e) {
+      for (int e = 0; e < 8; ++e) {
         o[2 * e] = fma_f32x2(y[e].x, f2, o[2 * e]);
         o[2 * e + 1] = fma_f32x2(y[e].y, f2, o[2 * e + 1]);
       }
     }
-    const float total = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const uint64_t t2 = pair_f32(total, total);
-#pragma unroll
-    for (int e = 0; e < kW / 2; ++e) o[e] = fma_f32x2(o[e], t2, 0ull);
-    pack_all();
-    store(w, c);
-    if (c == 0) store_lse();
+    emit(c, o);
   }
+  store_lse(mt, lt);
 }
 
 template <int kD, int kSrc>
@@ -995,13 +994,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         if (!row_wait(&S.ofin[L ^ 1], K & 1u, &S.abort_flag)) break;
       }
       tc_fence_after();
-      if (alt) {
-        row_output<kD, kD / 2, true>(p, S, it, warp, lane, 0, L * (kD / 2), true, o_base, tpt, m, l, f0, f1);
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < kD; c += 64)
-          row_output<kD, 64, false>(p, S, it, warp, lane, L, c, c + 64 == kD, o_base + kD * L, tpt, m, l, 1.f, 0.f);
-      }
+      if (alt) row_output<kD, true>(p, S, it, warp, lane, 0, L * (kD / 2), (L + 1) * (kD / 2), o_base, tpt, m, l, f0, f1);
+      else row_output<kD, false>(p, S, it, warp, lane, L, 0, kD, o_col, tpt, m, l, 1.f, 0.f);
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.iempty[slot]);
     }
