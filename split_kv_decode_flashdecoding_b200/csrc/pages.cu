@@ -136,54 +136,76 @@ __device__ __forceinline__ int64_t scan_array(int64_t* s, int n, int64_t* s_warp
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = 32;  // rows whose places one CTA looks up together
+constexpr int kAppendUnits = 4;  // units a lane has in flight
 
-// 16 destination bytes from the source elements at src.
+// The 16-byte loads that one 16-byte unit of the destination needs.
 template <typename S, bool kFp8>
-__device__ __forceinline__ uint4 append_unit(const S* src, float scale) {
+struct AppendUnit {
+  static constexpr int kLoads = kFp8 ? static_cast<int>(sizeof(S)) : 1;
+  uint4 v[kLoads];
+};
+
+template <typename S, bool kFp8>
+__device__ __forceinline__ void append_load(AppendUnit<S, kFp8>& a, const S* src) {
+#pragma unroll
+  for (int i = 0; i < AppendUnit<S, kFp8>::kLoads; ++i) a.v[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+}
+
+// x / s rounded to fp32 as the division rounds it: one Newton step on x times the rounded reciprocal r
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), for s
+// with a normal reciprocal. Quotients far beyond the largest code (and infinities, whose step would be
+// NaN) stay as the product gives them.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = x * r;
+  const float d = copysignf(fmaf(fmaf(-q, s, x), r, q), q);  // -0 keeps its sign
+  return fabsf(q) < 1e6f ? d : q;
+}
+
+template <typename S, bool kFp8>
+__device__ __forceinline__ uint4 append_convert(const AppendUnit<S, kFp8>& a, float scale, float recip) {
   if constexpr (!kFp8) {
-    return __ldg(reinterpret_cast<const uint4*>(src));
+    return a.v[0];
   } else {
     float x[16];
-    if constexpr (sizeof(S) == 4) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(src) + i);
-        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-      }
-    } else {
+    for (int i = 0; i < AppendUnit<S, kFp8>::kLoads; ++i) {
+      const uint32_t w[4] = {a.v[i].x, a.v[i].y, a.v[i].z, a.v[i].w};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // a bf16 is the upper half of the fp32 of the same value
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(S) == 4) {
+          x[4 * i + j] = __uint_as_float(w[j]);
+        } else {  // a bf16 is the upper half of the fp32 of the same value
           x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
           x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
         }
       }
     }
+    // a scale without a normal reciprocal (recip 0) divides
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = recip != 0.f ? quotient(x[i], scale, recip) : __fdiv_rn(x[i], scale);
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      uint32_t lo, hi;
-      const float a = __fdiv_rn(x[4 * i], scale), b = __fdiv_rn(x[4 * i + 1], scale);
-      const float c = __fdiv_rn(x[4 * i + 2], scale), d = __fdiv_rn(x[4 * i + 3], scale);
-      asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(lo) : "f"(a), "f"(b));
-      asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f32 t, %2, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(hi) : "f"(c), "f"(d));
-      o[i] = lo | (hi << 16);
+      asm("{\n\t.reg .b16 lo, hi;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+          "mov.b32 %0, {lo, hi};\n\t}"
+          : "=r"(o[i])
+          : "f"(x[4 * i]), "f"(x[4 * i + 1]), "f"(x[4 * i + 2]), "f"(x[4 * i + 3]));
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
 // A CTA takes p.rows_per_cta packed rows. Every thread sums new_lens (the ends of the sequences,
-// shared memory); one thread a row finds the row's sequence, page and slot; then all threads copy
-// the rows' K and V in 16-byte units of the destination.
+// shared memory); one thread a row finds the row's sequence, page and slot; then a warp takes a row, K
+// and V, in 16-byte units of the destination, four a lane in flight. Bound by HBM; E4M3 from bf16 by the
+// conversion's instructions as well (~8 a value).
 template <typename S, bool kFp8>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
   extern __shared__ int64_t s_end[];  // [batch] ends of the sequences' packed rows
   __shared__ int64_t s_warp[kAppendThreads / 32];
-  __shared__ int64_t s_k[kAppendRows], s_v[kAppendRows];  // element offset of the row's place, < 0: none
+  __shared__ int64_t s_place[kAppendRows];  // element offset of the row's place in both pools, < 0: none
   __shared__ int64_t s_total;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int64_t run = 0;
@@ -221,7 +243,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       const int b = upper_bound(s_end, p.batch, r);
       const int64_t start = b > 0 ? s_end[b - 1] : 0;
       const int64_t pos = static_cast<int64_t>(p.start_lens[b]) + (r - start);
-      int64_t place = -1, place_v = -1;
+      int64_t place = -1;
       if (p.start_lens[b] < 0 || pos >= cap) {
         atomicOr(p.status, FD_FLAG_LEN_CLAMPED);
       } else {
@@ -230,29 +252,39 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
           atomicOr(p.status, FD_FLAG_BAD_PAGE);
         } else {
           place = page * p.pool_sp + (pos % p.page_size) * p.d;
-          place_v = place;
         }
       }
-      s_k[tid] = place;
-      s_v[tid] = place_v;
+      s_place[tid] = place;
     }
     __syncthreads();
     const int per_head = p.d * (kFp8 ? 1 : static_cast<int>(sizeof(S))) / 16;  // a power of two
     const int shift = __ffs(per_head) - 1;
     const int elems = p.d / per_head;  // elements of one unit
     const int half = p.hkv * per_head;
-    for (int i = 0; i < n; ++i) {
-      if (s_k[i] < 0) continue;
-      for (int u = tid; u < 2 * half; u += kAppendThreads) {
-        const bool is_v = u >= half;
-        const int w = is_v ? u - half : u;
-        const int h = w >> shift, e = (w & (per_head - 1)) * elems;
-        const S* src = is_v ? static_cast<const S*>(p.v_new) + (r0 + i) * p.v_sr + h * p.v_sh + e
-                            : static_cast<const S*>(p.k_new) + (r0 + i) * p.k_sr + h * p.k_sh + e;
-        const uint4 x = append_unit<S, kFp8>(src, is_v ? p.v_scale : p.k_scale);
-        const int64_t at = (is_v ? s_v[i] : s_k[i]) + h * p.pool_sh + e;
-        char* dst = static_cast<char*>(is_v ? p.v_pages : p.k_pages) + at * (kFp8 ? 1 : static_cast<int>(sizeof(S)));
-        *reinterpret_cast<uint4*>(dst) = x;
+    for (int i = warp; i < n; i += kAppendThreads / 32) {
+      const int64_t place = s_place[i];
+      if (place < 0) continue;
+      const S* k_row = static_cast<const S*>(p.k_new) + (r0 + i) * p.k_sr;
+      const S* v_row = static_cast<const S*>(p.v_new) + (r0 + i) * p.v_sr;
+      for (int u0 = lane; u0 < 2 * half; u0 += 32 * kAppendUnits) {
+        AppendUnit<S, kFp8> x[kAppendUnits];
+#pragma unroll
+        for (int j = 0; j < kAppendUnits; ++j) {
+          const int u = u0 + 32 * j, w = u >= half ? u - half : u;
+          const int h = w >> shift, e = (w & (per_head - 1)) * elems;
+          if (u < 2 * half) append_load(x[j], u >= half ? v_row + h * p.v_sh + e : k_row + h * p.k_sh + e);
+        }
+#pragma unroll
+        for (int j = 0; j < kAppendUnits; ++j) {
+          const int u = u0 + 32 * j, w = u >= half ? u - half : u;
+          const int h = w >> shift, e = (w & (per_head - 1)) * elems;
+          if (u < 2 * half) {
+            const uint4 c = append_convert(x[j], u >= half ? p.v_scale : p.k_scale, u >= half ? p.v_recip : p.k_recip);
+            char* dst = static_cast<char*>(u >= half ? p.v_pages : p.k_pages) +
+                        (place + h * p.pool_sh + e) * (kFp8 ? 1 : static_cast<int>(sizeof(S)));
+            *reinterpret_cast<uint4*>(dst) = c;
+          }
+        }
       }
     }
     __syncthreads();
@@ -482,7 +514,7 @@ __device__ __forceinline__ bool check_compact(const CompactParams& p, int b, int
 // Block (b, j): moves the rows of K (j even) or V, KV head j / 2, of sequence b. The list increases
 // strictly, so a row read lies at or behind the row written for it and behind every row written for
 // an earlier one: kMove rows a thread are read, then (after a barrier) written, front to back.
-constexpr int kMove = 4;
+constexpr int kMove = 8;
 __global__ void __launch_bounds__(kCompactThreads) compact_move_kernel(const CompactParams p) {
   const int b = blockIdx.x, tid = threadIdx.x;
   const int m = p.keep_lens[b];

@@ -121,6 +121,12 @@ fd_status append(const fd_tensor* k_new, const fd_tensor* v_new, fd_tensor* k, f
   p.d = static_cast<int32_t>(k->shape[3]);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  const auto recip = [](float s) {
+    const float r = 1.f / s;
+    return s >= FLT_MIN && r >= FLT_MIN && r <= FLT_MAX ? r : 0.f;
+  };
+  p.k_recip = recip(k_scale);
+  p.v_recip = recip(v_scale);
   p.status = reinterpret_cast<uint32_t*>(ws);
   return launched(launch_append(p, k_new->dtype, fp8, nsm, stream), "append kernel launch");
 }

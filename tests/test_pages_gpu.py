@@ -117,7 +117,7 @@ def test_append_skips_what_has_no_place():
 @pytest.mark.parametrize("d", [64, 128])
 def test_append_fp8(src, d):
     fd = _fd()
-    for scale in (1.0, 0.37, 1e-3):
+    for scale in (1.0, 0.37, 1e-3, 1e-38, 1e-40, 1e30):
         s = Both(20, 2, 32, d, 3, 8, torch.uint8)
         s.reserve([40, 3, 64])
         x = torch.randn((2, 107, 2, d), generator=s.gen, device="cuda") * 100
