@@ -42,20 +42,21 @@ __device__ __forceinline__ T block_scan(T v, T* s_warp, T* total) {
   return warp > 0 ? v + s_warp[warp - 1] : v;
 }
 
-// Leading non-negative entries among row[0, limit), by one warp (the same value in every lane).
+// Leading non-negative entries among row[0, limit), by one warp (the same value in every lane); 256
+// entries are in flight.
 __device__ __forceinline__ int leading_pages(const int32_t* row, int limit) {
   const int lane = threadIdx.x & 31;
-  for (int c0 = 0; c0 < limit; c0 += 128) {
-    int32_t e[4];
+  for (int c0 = 0; c0 < limit; c0 += 256) {
+    int32_t e[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const int c = c0 + 32 * k + lane;
-      e[k] = c < limit ? row[c] : -1;
+      e[k] = c < limit ? row[c] : 0;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 8; ++k) {
       const unsigned neg = __ballot_sync(0xffffffffu, e[k] < 0);
-      if (neg) return min(limit, c0 + 32 * k + __ffs(neg) - 1);
+      if (neg) return c0 + 32 * k + __ffs(neg) - 1;
     }
   }
   return limit;
@@ -136,7 +137,9 @@ __device__ __forceinline__ int64_t scan_array(int64_t* s, int n, int64_t* s_warp
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = 32;  // rows whose places one CTA looks up together
-constexpr int kAppendUnits = 4;  // units a lane has in flight
+// Units a lane has in flight. E4M3 from bf16: two keep 4 CTAs resident (four: 97 registers, 2 CTAs).
+template <bool kFp8>
+constexpr int kAppendUnits = kFp8 ? 2 : 4;
 
 // The 16-byte loads that one 16-byte unit of the destination needs.
 template <typename S, bool kFp8>
@@ -207,7 +210,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
   __shared__ int64_t s_warp[kAppendThreads / 32];
   __shared__ int64_t s_place[kAppendRows];  // element offset of the row's place in both pools, < 0: none
   __shared__ int64_t s_total;
+  constexpr int kUnits = kAppendUnits<kFp8>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
   int64_t run = 0;
   for (int i0 = 0; i0 < p.batch; i0 += kAppendThreads) {
     const int i = i0 + tid;
@@ -266,16 +272,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
       if (place < 0) continue;
       const S* k_row = static_cast<const S*>(p.k_new) + (r0 + i) * p.k_sr;
       const S* v_row = static_cast<const S*>(p.v_new) + (r0 + i) * p.v_sr;
-      for (int u0 = lane; u0 < 2 * half; u0 += 32 * kAppendUnits) {
-        AppendUnit<S, kFp8> x[kAppendUnits];
+      for (int u0 = lane; u0 < 2 * half; u0 += 32 * kUnits) {
+        AppendUnit<S, kFp8> x[kUnits];
 #pragma unroll
-        for (int j = 0; j < kAppendUnits; ++j) {
+        for (int j = 0; j < kUnits; ++j) {
           const int u = u0 + 32 * j, w = u >= half ? u - half : u;
           const int h = w >> shift, e = (w & (per_head - 1)) * elems;
           if (u < 2 * half) append_load(x[j], u >= half ? v_row + h * p.v_sh + e : k_row + h * p.k_sh + e);
         }
 #pragma unroll
-        for (int j = 0; j < kAppendUnits; ++j) {
+        for (int j = 0; j < kUnits; ++j) {
           const int u = u0 + 32 * j, w = u >= half ? u - half : u;
           const int h = w >> shift, e = (w & (per_head - 1)) * elems;
           if (u < 2 * half) {
@@ -293,7 +299,9 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 
 // ---- reserve --------------------------------------------------------------------------------------
 
-// One CTA. A warp a sequence counts its pages; the missing ones, summed over the sequences, are the
+constexpr int kRowsAtOnce = 4;
+
+// One CTA. A warp counts the pages of four sequences at a time; the missing ones, summed over the sequences, are the
 // ranks of the free pages that visit_free_pages gives. If they run out, the sequences whose sum
 // exceeds what there was give back what they got.
 __global__ void __launch_bounds__(kTableThreads) reserve_kernel(const ReserveParams p) {
@@ -302,17 +310,53 @@ __global__ void __launch_bounds__(kTableThreads) reserve_kernel(const ReservePar
   __shared__ int64_t s_warp[32];
   __shared__ unsigned long long s_warp2[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int b = warp; b < p.batch; b += kTableThreads / 32) {
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
+  // the pages wanted, a thread a sequence; then what stands in the rows, a warp kRowsAtOnce rows together
+  for (int b = threadIdx.x; b < p.batch; b += kTableThreads) {
     int64_t want = (max(static_cast<int64_t>(p.want_lens[b]), int64_t(0)) + p.page_size - 1) / p.page_size;
     if (want > p.pages_per_seq) {
       want = p.pages_per_seq;
-      if (lane == 0) atomicOr(p.status, FD_FLAG_LEN_CLAMPED);
+      atomicOr(p.status, FD_FLAG_LEN_CLAMPED);
     }
-    const int have = leading_pages(p.block_table + static_cast<int64_t>(b) * p.pages_per_seq, static_cast<int>(want));
-    if (lane == 0) {
-      s_have[b] = have;
-      s_sum[b] = want - have;
+    s_have[b] = static_cast<int32_t>(want);
+    s_sum[b] = want;
+  }
+  __syncthreads();
+  for (int b0 = warp * kRowsAtOnce; b0 < p.batch; b0 += kTableThreads / 32 * kRowsAtOnce) {
+    int most = 0, limit[kRowsAtOnce];
+#pragma unroll
+    for (int i = 0; i < kRowsAtOnce; ++i) {
+      limit[i] = b0 + i < p.batch ? s_have[b0 + i] : 0;
+      most = max(most, limit[i]);
     }
+    int have[kRowsAtOnce];
+#pragma unroll
+    for (int i = 0; i < kRowsAtOnce; ++i) have[i] = limit[i];
+    for (int c0 = 0; c0 < most; c0 += 64) {
+      int32_t e[kRowsAtOnce][2];
+#pragma unroll
+      for (int i = 0; i < kRowsAtOnce; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int c = c0 + 32 * k + lane;
+          e[i][k] = c < limit[i] ? p.block_table[static_cast<int64_t>(b0 + i) * p.pages_per_seq + c] : 0;
+        }
+#pragma unroll
+      for (int i = 0; i < kRowsAtOnce; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const unsigned neg = __ballot_sync(0xffffffffu, e[i][k] < 0);
+          if (neg) have[i] = min(have[i], c0 + 32 * k + __ffs(neg) - 1);
+        }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kRowsAtOnce; ++i)
+      if (lane == 0 && b0 + i < p.batch) {
+        s_have[b0 + i] = have[i];
+        s_sum[b0 + i] -= have[i];
+      }
   }
   __syncthreads();
   const int64_t need = scan_array(s_sum, p.batch, s_warp);
@@ -349,6 +393,8 @@ __global__ void __launch_bounds__(kTableThreads) fork_plan_kernel(const ForkPara
   __shared__ int64_t s_warp[32];
   __shared__ unsigned long long s_warp2[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
   for (int b = threadIdx.x; b < p.batch; b += kTableThreads) s_owner[b] = INT32_MAX;
   __syncthreads();
   for (int i = threadIdx.x; i < p.count; i += kTableThreads) {
@@ -368,8 +414,20 @@ __global__ void __launch_bounds__(kTableThreads) fork_plan_kernel(const ForkPara
       const int64_t pages = (static_cast<int64_t>(len) + p.page_size - 1) / p.page_size;
       bool ok = len >= 0 && pages <= p.pages_per_seq;
       const int32_t* row = p.block_table + static_cast<int64_t>(src) * p.pages_per_seq;
-      for (int64_t c = lane; ok && c < pages; c += 32)
-        ok = row[c] >= 0 && row[c] < p.num_pages && p.page_refs[row[c]] > 0;
+      for (int64_t c0 = 0; ok && c0 < pages; c0 += 256) {
+        int32_t e[8], f[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int64_t c = c0 + 32 * k + lane;
+          e[k] = c < pages ? row[c] : -1;
+          f[k] = c < pages ? 0 : 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (e[k] >= 0 && e[k] < p.num_pages) f[k] = p.page_refs[e[k]];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ok = ok && f[k] > 0;
+      }
       if (!__all_sync(0xffffffffu, ok)) {
         len = -1;
         flag = FD_FLAG_BAD_PAGE;
@@ -397,16 +455,19 @@ __global__ void __launch_bounds__(kTableThreads) fork_plan_kernel(const ForkPara
       const int full = len / p.page_size;
       const int32_t* from = p.block_table + static_cast<int64_t>(src) * p.pages_per_seq;
       int32_t* to = p.block_table + static_cast<int64_t>(dst) * p.pages_per_seq;
-      for (int c = lane; c < p.pages_per_seq; c += 32) {
-        int32_t page = -1;
-        if (c < full) {
-          page = from[c];
-          atomicAdd(&p.page_refs[page], 1);
-        } else if (c == full && fresh) {
-          page = s_page[i];
-          atomicAdd(&p.page_refs[page], 1);
+      for (int c0 = 0; c0 < p.pages_per_seq; c0 += 128) {
+        int32_t page[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = c0 + 32 * k + lane;
+          page[k] = c < full ? from[c] : c == full && fresh ? s_page[i] : -1;
         }
-        to[c] = page;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = c0 + 32 * k + lane;
+          if (c < p.pages_per_seq) to[c] = page[k];
+          if (page[k] >= 0) atomicAdd(&p.page_refs[page[k]], 1);
+        }
       }
       if (lane == 0) {
         p.cache_lens[dst] = len;
@@ -421,6 +482,8 @@ constexpr int kCopyThreads = 256;
 
 // Block (i, j): the K (j even) or V rows of KV head j / 2 of copy i, contiguous in both pages.
 __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const ForkParams p) {
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
   const int4 c = p.copies[blockIdx.x];
   if (c.z == 0) return;
   const int h = blockIdx.y >> 1;
@@ -428,7 +491,15 @@ __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const ForkParam
   const uint4* src = reinterpret_cast<const uint4*>(pool + c.x * p.pool_sp + h * p.pool_sh);
   uint4* dst = reinterpret_cast<uint4*>(pool + c.y * p.pool_sp + h * p.pool_sh);
   const int64_t n = static_cast<int64_t>(c.z) * p.row_bytes / 16;
-  for (int64_t u = threadIdx.x; u < n; u += kCopyThreads) dst[u] = src[u];
+  for (int64_t u0 = threadIdx.x; u0 < n; u0 += 8 * kCopyThreads) {
+    uint4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (u0 + k * kCopyThreads < n) x[k] = src[u0 + k * kCopyThreads];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (u0 + k * kCopyThreads < n) dst[u0 + k * kCopyThreads] = x[k];
+  }
 }
 
 // ---- free -----------------------------------------------------------------------------------------
@@ -438,6 +509,8 @@ constexpr int kFreeThreads = 128;
 // One CTA a listed sequence; the first of equal entries frees it.
 __global__ void __launch_bounds__(kFreeThreads) free_kernel(const FreeParams p) {
   const int i = blockIdx.x, tid = threadIdx.x;
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
   const int b = p.seqs[i];
   if (b < 0 || b >= p.batch) {
     if (tid == 0) atomicOr(p.status, FD_FLAG_BAD_INDEX);
@@ -511,49 +584,80 @@ __device__ __forceinline__ bool check_compact(const CompactParams& p, int b, int
   return true;
 }
 
-// Block (b, j): moves the rows of K (j even) or V, KV head j / 2, of sequence b. The list increases
-// strictly, so a row read lies at or behind the row written for it and behind every row written for
-// an earlier one: kMove rows a thread are read, then (after a barrier) written, front to back.
+// Block (b, j): moves the rows of K (j even) or V, KV head j / 2, of sequence b, a batch of kMove rows a
+// thread after the other. The list increases strictly, so a row read lies at or behind the row written for
+// it: rows read for a later batch lie behind every row written for an earlier one. A batch's rows are
+// therefore loaded before the batch before it is stored, and only a batch's own loads and stores need the
+// barrier between them. The places of a batch are looked up two or three batches ahead, one
+// thread a row, in a ring of four.
 constexpr int kMove = 8;
+constexpr int kMoveRows = kMove * kCompactThreads / 4;  // rows of a batch at most (64-byte rows)
 __global__ void __launch_bounds__(kCompactThreads) compact_move_kernel(const CompactParams p) {
+  __shared__ int64_t s_from[4][kMoveRows], s_to[4][kMoveRows];
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
   const int b = blockIdx.x, tid = threadIdx.x;
   const int m = p.keep_lens[b];
   int first = 0;
   const bool go = m >= 0 && check_compact(p, b, m, &first, blockIdx.y == 0);
   if (blockIdx.y == 0 && tid == 0) p.valid[b] = go ? 1 : 0;
-  if (!go) return;
+  if (!go || first >= m) return;
   const int h = blockIdx.y >> 1;
   char* pool = static_cast<char*>((blockIdx.y & 1) ? p.v_pages : p.k_pages) + h * p.pool_sh;
   const int units = p.row_bytes / 16;  // 4 .. 32, a power of two
-  const int per = kCompactThreads / units;
+  const int per = kCompactThreads / units, batch = kMove * per;
   const int unit = tid & (units - 1), slot = tid / units;
   const int32_t start = p.start_lens[b];
   const int32_t* keep = p.keep + static_cast<int64_t>(b) * p.max_keep;
   const int32_t* row = p.block_table + static_cast<int64_t>(b) * p.pages_per_seq;
   auto at = [&](int pos) {
-    return reinterpret_cast<uint4*>(pool + row[pos / p.page_size] * p.pool_sp +
-                                    static_cast<int64_t>(pos % p.page_size) * p.row_bytes) + unit;
+    return row[pos / p.page_size] * p.pool_sp + static_cast<int64_t>(pos % p.page_size) * p.row_bytes;
   };
-  for (int i0 = first; i0 < m; i0 += kMove * per) {
-    uint4 x[kMove];
-#pragma unroll
-    for (int k = 0; k < kMove; ++k) {
-      const int i = i0 + k * per + slot;
-      if (i < m) x[k] = *at(start + keep[i]);
+  auto look_up = [&](int n) {  // the places of batch n
+    for (int k = tid; k < batch; k += kCompactThreads) {
+      const int i = first + n * batch + k;
+      if (i < m) {
+        s_from[n & 3][k] = at(start + keep[i]);
+        s_to[n & 3][k] = at(start + i);
+      }
     }
-    __syncthreads();
+  };
+  auto load = [&](int n, uint4 (&x)[kMove]) {
 #pragma unroll
-    for (int k = 0; k < kMove; ++k) {
-      const int i = i0 + k * per + slot;
-      if (i < m) *at(start + i) = x[k];
-    }
+    for (int k = 0; k < kMove; ++k)
+      if (first + n * batch + k * per + slot < m)
+        x[k] = reinterpret_cast<const uint4*>(pool + s_from[n & 3][k * per + slot])[unit];
+  };
+  auto store = [&](int n, const uint4 (&x)[kMove]) {
+#pragma unroll
+    for (int k = 0; k < kMove; ++k)
+      if (first + n * batch + k * per + slot < m) reinterpret_cast<uint4*>(pool + s_to[n & 3][k * per + slot])[unit] = x[k];
+  };
+  const int batches = (m - first + batch - 1) / batch;
+  uint4 x[kMove], y[kMove];
+  look_up(0);
+  if (batches > 1) look_up(1);
+  __syncthreads();
+  load(0, x);
+  // two batches a round, so that the registers keep their roles
+  for (int n = 0; n < batches; n += 2) {
+    if (n + 1 < batches) load(n + 1, y);
+    if (n + 2 < batches) look_up(n + 2);
+    __syncthreads();  // everyone has loaded batch n (and n + 1)
+    store(n, x);
+    if (n + 1 >= batches) break;
+    if (n + 2 < batches) load(n + 2, x);
+    if (n + 3 < batches) look_up(n + 3);
     __syncthreads();
+    store(n + 1, y);
   }
 }
 
 // One CTA a sequence: the new length, the pages behind it given back.
 __global__ void __launch_bounds__(kFreeThreads) compact_table_kernel(const CompactParams p) {
   const int b = blockIdx.x, tid = threadIdx.x;
+  pdl_launch_dependents();
+  pdl_wait_prerequisites();
   const int m = p.keep_lens[b];
   if (m < 0 || !p.valid[b]) return;
   const int64_t len = static_cast<int64_t>(p.start_lens[b]) + m;
@@ -577,10 +681,26 @@ __global__ void __launch_bounds__(kFreeThreads) compact_table_kernel(const Compa
 
 // ---- launchers ------------------------------------------------------------------------------------
 
-template <typename S, bool kFp8>
-static cudaError_t launch_append_t(const AppendParams& p, int grid, cudaStream_t stream) {
-  append_kernel<S, kFp8><<<grid, kAppendThreads, sizeof(int64_t) * p.batch, stream>>>(p);
-  return cudaGetLastError();
+// Launched with programmatic stream serialization: a kernel becomes resident while the one before it
+// runs, and waits for it before it reads or writes anything.
+template <typename P>
+static cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 cudaError_t launch_append(AppendParams p, int src_dtype, bool fp8, int nsm, cudaStream_t stream) {
@@ -588,45 +708,30 @@ cudaError_t launch_append(AppendParams p, int src_dtype, bool fp8, int nsm, cuda
   p.rows_per_cta = static_cast<int>(want < 1 ? 1 : want > kAppendRows ? kAppendRows : want);
   int64_t grid = (p.rows + p.rows_per_cta - 1) / p.rows_per_cta;
   if (grid > 16 * nsm) grid = 16 * nsm;
-  const int g = static_cast<int>(grid);
-  if (src_dtype == FD_F32) return fp8 ? launch_append_t<float, true>(p, g, stream) : launch_append_t<float, false>(p, g, stream);
-  return fp8 ? launch_append_t<__nv_bfloat16, true>(p, g, stream) : launch_append_t<__nv_bfloat16, false>(p, g, stream);
-}
-
-static cudaError_t allow_smem(const void* f, size_t bytes) {
-  return bytes <= 48 * 1024 ? cudaSuccess
-                            : cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  void (*kernel)(AppendParams) = src_dtype == FD_F32 ? (fp8 ? append_kernel<float, true> : append_kernel<float, false>)
+                                                     : (fp8 ? append_kernel<__nv_bfloat16, true> : append_kernel<__nv_bfloat16, false>);
+  return launch(kernel, dim3(static_cast<unsigned>(grid)), kAppendThreads, sizeof(int64_t) * p.batch, stream, p);
 }
 
 cudaError_t launch_reserve(const ReserveParams& p, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(p.batch) * 12;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(reserve_kernel), smem);
-  if (e != cudaSuccess) return e;
-  reserve_kernel<<<1, kTableThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch(reserve_kernel, dim3(1), kTableThreads, static_cast<size_t>(p.batch) * 12, stream, p);
 }
 
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
   const size_t smem = static_cast<size_t>(p.count) * 16 + static_cast<size_t>(p.batch) * 4;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fork_plan_kernel), smem);
+  const cudaError_t e = launch(fork_plan_kernel, dim3(1), kTableThreads, smem, stream, p);
   if (e != cudaSuccess) return e;
-  fork_plan_kernel<<<1, kTableThreads, smem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  fork_copy_kernel<<<dim3(p.count, 2 * p.hkv), kCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch(fork_copy_kernel, dim3(p.count, 2 * p.hkv), kCopyThreads, 0, stream, p);
 }
 
 cudaError_t launch_free(const FreeParams& p, cudaStream_t stream) {
-  free_kernel<<<p.count, kFreeThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch(free_kernel, dim3(p.count), kFreeThreads, 0, stream, p);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
-  compact_move_kernel<<<dim3(p.batch, 2 * p.hkv), kCompactThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch(compact_move_kernel, dim3(p.batch, 2 * p.hkv), kCompactThreads, 0, stream, p);
   if (e != cudaSuccess) return e;
-  compact_table_kernel<<<p.batch, kFreeThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch(compact_table_kernel, dim3(p.batch), kFreeThreads, 0, stream, p);
 }
 
 }  // namespace fd

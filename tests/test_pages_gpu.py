@@ -206,6 +206,10 @@ def test_fork_refuses():
     s.fork([1, 0], [4, 5])
     s.same(fd.FD_FLAG_BAD_PAGE)
     assert s.host.lens == [20, 8, 20, 0, 0, 20]
+    s.table[1, 0] = -2                                # any negative entry is none
+    s.host.table[1][0] = -2
+    s.fork([1], [4])
+    s.same(fd.FD_FLAG_BAD_PAGE)
 
 
 def test_fork_when_pages_run_out():
@@ -256,6 +260,17 @@ def test_compact_of_a_long_list():
     g = torch.Generator().manual_seed(6)
     keep = [torch.randperm(5000, generator=g)[:3333].sort().values.tolist(), [9], list(range(1, 4096))]
     s.compact([0, 0, 0], keep)
+    s.same()
+
+
+@pytest.mark.parametrize("shift", [1, 127, 128, 129, 500])
+def test_compact_that_closes_one_gap(shift):
+    # every row moves by the same distance, below, at and above the rows that move together
+    s = Both(300, 1, 16, 128, 2, 260)
+    n = 1500
+    s.reserve([n + shift, 0])
+    s.append([0, 0], [n + shift, 0])
+    s.compact([0, 0], [list(range(shift, n + shift)), None])
     s.same()
 
 
