@@ -29,14 +29,14 @@ struct RowsParams {
   float scale_log2;                // log2(e) / sqrt(D)
   int32_t g_recip16;               // ceil(2^16 / G): (r * g_recip16) >> 16 == r / G for 0 <= r < 128
   int32_t q_box_rows;              // tokens of one Q box (G heads each): min(128 / G, rows)
-  int32_t kv_box_rows;             // rows of one K/V box
+  int32_t kv_box_rows;             // keys of one K or V box: min(128; rows, S_cap or page_size)
   WsHeader* hdr;
   float *part_o, *part_ml;         // pieces of cut items, behind the header (launch_rows)
 };
 
 // tcgen05 kernel: bf16, D 64 or 128, G <= 16. Maps: q as (D, Hq, rows), box 64 x G x q_box_rows; k and v
-// as (D, Hkv, rows) with box 64 x 1 x kv_box_rows (prompt), (D, S_cap, Hkv, B) or (D, page_size, Hkv,
-// num_pages) with box 64 x kv_box_rows x 1 x 1.
+// as (D, Hkv, rows) with box 64 x 1 x box rows (prompt), (D, S_cap, Hkv, B) or (D, page_size, Hkv,
+// num_pages) with box 64 x box rows x 1 x 1.
 size_t rows_workspace_bytes(int d, int nctas);
 cudaError_t launch_rows(RowsParams p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int nctas,
                         cudaStream_t stream);

@@ -59,9 +59,10 @@ fd_status resolve_rows(const fd_tensor* q, const fd_tensor* out, int64_t hkv, in
 
 int row_ctas(int nsm) { return std::min(nsm, kMaxRowCtas); }
 
-// Launch on all multiprocessors. kd / ks: dimensions and byte strides of the K map (ksv: of the V map).
+// Launch on all multiprocessors. kd: dimensions of the K and V maps, ks / vs their byte strides; kv_rows: keys
+// that one box may reach over.
 fd_status run_rows(RowsParams* p, int kv_rank, const uint64_t* kd, const uint64_t* ks, const uint64_t* vs,
-                   const uint32_t* kb, cudaStream_t stream) {
+                   int kv_rows, cudaStream_t stream) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -77,6 +78,9 @@ fd_status run_rows(RowsParams* p, int kv_rank, const uint64_t* kd, const uint64_
   const uint64_t qs[2] = {static_cast<uint64_t>(p->q_sh) * 2, static_cast<uint64_t>(p->q_sr) * 2};
   const uint32_t qb[3] = {64, static_cast<uint32_t>(p->g), static_cast<uint32_t>(p->q_box_rows)};
   if ((s = make_tmap(&tq, p->q, 3, qd, qs, qb, "q")) != FD_OK) return s;
+  p->kv_box_rows = std::min(128, kv_rows);
+  uint32_t kb[4] = {64, 1, 1, 1};
+  kb[kv_rank == 3 ? 2 : 1] = static_cast<uint32_t>(p->kv_box_rows);
   if ((s = make_tmap(&tk, p->k, kv_rank, kd, ks, kb, "k")) != FD_OK) return s;
   if ((s = make_tmap(&tv, p->v, kv_rank, kd, vs, kb, "v")) != FD_OK) return s;
   e = launch_rows(*p, tq, tk, tv, nctas, stream);
@@ -136,13 +140,11 @@ fd_status tree(const fd_tensor* q, const fd_tensor* k, const fd_tensor* v, const
   p.prefix_lens = prefix_lens;
   p.mask = reinterpret_cast<const uint32_t*>(tree_mask);
   p.mask_words = mask_words;
-  p.kv_box_rows = std::min(128, paged ? p.page_size : p.cap);
   const uint64_t kd[4] = {static_cast<uint64_t>(p.d), static_cast<uint64_t>(k->shape[2]), static_cast<uint64_t>(p.hkv),
                           static_cast<uint64_t>(k->shape[0])};
   const uint64_t ks[3] = {static_cast<uint64_t>(k->stride[2]) * 2, static_cast<uint64_t>(k->stride[1]) * 2,
                           static_cast<uint64_t>(k->stride[0]) * 2};
-  const uint32_t kb[4] = {64, static_cast<uint32_t>(p.kv_box_rows), 1, 1};
-  return run_rows(&p, 4, kd, ks, ks, kb, stream);
+  return run_rows(&p, 4, kd, ks, ks, paged ? p.page_size : p.cap, stream);
 }
 
 }  // namespace
@@ -171,12 +173,10 @@ fd_status fd_prompt_attention(const fd_tensor* q, const fd_tensor* k, const fd_t
   p.lse = lse;
   p.row_lens = seq_lens;
   p.cap = p.rows;
-  p.kv_box_rows = std::min(128, p.rows);
   const uint64_t kd[3] = {static_cast<uint64_t>(p.d), static_cast<uint64_t>(p.hkv), static_cast<uint64_t>(p.rows)};
   const uint64_t ks[2] = {static_cast<uint64_t>(p.k_sh) * 2, static_cast<uint64_t>(p.k_sr) * 2};
   const uint64_t vs[2] = {static_cast<uint64_t>(p.v_sh) * 2, static_cast<uint64_t>(p.v_sr) * 2};
-  const uint32_t kb[3] = {64, 1, static_cast<uint32_t>(p.kv_box_rows)};
-  return run_rows(&p, 3, kd, ks, vs, kb, static_cast<cudaStream_t>(stream));
+  return run_rows(&p, 3, kd, ks, vs, p.rows, static_cast<cudaStream_t>(stream));
 }
 
 fd_status fd_tree_attention(const fd_tensor* q, const fd_tensor* k_cache, const fd_tensor* v_cache,

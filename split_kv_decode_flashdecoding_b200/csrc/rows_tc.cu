@@ -27,7 +27,7 @@
 // which one that is.
 //
 // Warps: 0-3 and 4-7 softmax and output of lanes 0 and 1 (warp w reads TMEM lanes 32 (w mod 4) + [0, 32),
-// one row a thread); 8 plan and TMA; 9 tensor-core issue.
+// one row a thread); 8 plan and TMA of Q and K; 9 tensor-core issue; 10 TMA of V.
 #include <type_traits>
 
 #include "common.cuh"
@@ -39,10 +39,10 @@ namespace fd {
 namespace {
 
 constexpr int kRwThreads = 12 * 32;
-constexpr int kRwProducer = 8, kRwIssue = 9;
+constexpr int kRwProducer = 8, kRwIssue = 9, kRwVProducer = 10;
 constexpr int kRwItems = 4;                    // item descriptors in flight
 constexpr uint32_t kRwTmemCols = 512;
-constexpr uint32_t kRwColO = 256;              // O of lane L at kRwColO + L D; S / P of lane L at 128 L
+constexpr uint32_t kRwColO = 256;              // O of lane L at kRwColO + L D; S, then P, of lane L at 128 L
 constexpr uint32_t kRwHalf = 128 * 64 * 2;     // bytes of one 64-column half of a 128-row tile
 constexpr float kRwRescale = 8.0f;             // log2 units
 constexpr uint32_t kRwWaitClocks = 0x80000000u;
@@ -67,9 +67,11 @@ struct RowItem {
 template <int kD>
 struct __align__(1024) RwSmem {
   static constexpr int kHalves = kD / 64;
-  static constexpr int kStages = kD == 128 ? 4 : 8;  // K and V tiles alternate
+  static constexpr int kKStages = kD == 128 ? 2 : 4;  // of K and of V
+  static constexpr int kVStages = kKStages;
   __nv_bfloat16 q[2][kHalves][128 * 64];
-  __nv_bfloat16 kv[kStages][kHalves][128 * 64];
+  __nv_bfloat16 k[kKStages][kHalves][128 * 64];
+  __nv_bfloat16 v[kVStages][kHalves][128 * 64];
   RowItem item[kRwItems];
   float2 xend[8][32];  // softmax warps: a row's (m, l) at the end of an alt item, for the other lane's warp
   union {
@@ -79,9 +81,10 @@ struct __align__(1024) RwSmem {
     };
     uint4 stage[8][128];  // output: a warp's rows, 32 columns
   };
-  uint64_t full[kStages], empty[kStages];
+  uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages];
   uint64_t qfull[2], qempty[2], ifull[kRwItems], iempty[kRwItems];
-  uint64_t sfull[2], pfull[2][2], ofin[2], oempty[2];  // pfull: keys [0, 64) and [64, 128)
+  // by lane: a tile's scores are there, P of keys [0, 64) and of [64, 128) is stored, O is complete, is read
+  uint64_t sfull[2], pfull[2][2], ofin[2], oempty[2];
   uint64_t xpair[4];  // exchanges of the two lanes' warps of a row quarter (alt items)
   uint64_t drain;
   uint32_t tmem_base;
@@ -336,13 +339,56 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
   store_lse(mt, lt);
 }
 
+// The copies of a tile of K or V into one stage, one box a lane: the box's page and 64-column half
+// (paged), or its half.
+template <int kD, int kSrc>
+struct KeyBoxes {
+  static constexpr int kHalves = kD / 64, kKeys = 128;
+  int psz, boxes, box_page, box_half, lane, h, b, row0, k1;
+  __device__ __forceinline__ KeyBoxes(const RowsParams& p, const RowItem& it, int lane_) {
+    lane = lane_;
+    psz = kSrc == kSrcPaged ? min(p.page_size, kKeys) : kKeys;
+    boxes = (kKeys / psz) * kHalves;
+    box_page = lane / kHalves;
+    box_half = lane % kHalves;
+    h = it.h;
+    b = it.b;
+    row0 = it.key_row0;
+    k1 = it.k1;
+  }
+  // the page of this lane's box in piece `n` (keys [n kKeys, (n + 1) kKeys)) of the request
+  __device__ __forceinline__ int page(const RowsParams& p, int n) const {
+    if constexpr (kSrc == kSrcPaged) {
+      const int key = n * kKeys + box_page * psz;
+      if (lane < boxes && key < k1) {
+        const int id = p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + key / p.page_size];
+        if (id >= 0 && id < p.num_pages) return id;
+        atomicOr(&p.hdr->status, FD_FLAG_BAD_PAGE);
+      }
+      return p.num_pages;  // outside the map: the copy writes zeros
+    }
+    return 0;
+  }
+  __device__ __forceinline__ void load(const RowsParams& p, const CUtensorMap* map, uint64_t* full, __nv_bfloat16* stage,
+                                       int n, int page) const {
+    if (lane == 0) mbar_arrive_expect_tx(full, kHalves * 128u * static_cast<uint32_t>(p.kv_box_rows * (kKeys / psz)));
+    __syncwarp();
+    if (lane < boxes) {
+      __nv_bfloat16* dst = stage + box_half * kKeys * 64 + box_page * psz * 64;
+      if constexpr (kSrc == kSrcPacked) tma_load_3d(dst, map, full, 64 * box_half, h, row0 + n * kKeys);
+      else if constexpr (kSrc == kSrcCache) tma_load_4d(dst, map, full, 64 * box_half, n * kKeys, h, b);
+      else tma_load_4d(dst, map, full, 64 * box_half, n * kKeys % p.page_size, h, page);
+    }
+  }
+};
+
 template <int kD, int kSrc>
 __global__ void __launch_bounds__(kRwThreads, 1)
     rows_tc_kernel(const RowsParams p, const __grid_constant__ CUtensorMap tmap_q,
                    const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v) {
   using Smem = RwSmem<kD>;
   constexpr bool kCausal = kSrc == kSrcPacked;
-  constexpr int kHalves = Smem::kHalves, kStages = Smem::kStages;
+  constexpr int kHalves = Smem::kHalves, kKStages = Smem::kKStages, kVStages = Smem::kVStages;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31;
@@ -350,13 +396,17 @@ __global__ void __launch_bounds__(kRwThreads, 1)
   const int tpt = rows_tile_tokens(p.g);
 
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&S.full[s], 1);
-      mbar_init(&S.empty[s], 2);  // both lanes' products
+    for (int s = 0; s < Smem::kKStages; ++s) {
+      mbar_init(&S.kfull[s], 1);
+      mbar_init(&S.kempty[s], 2);  // both lanes' products
+    }
+    for (int s = 0; s < Smem::kVStages; ++s) {
+      mbar_init(&S.vfull[s], 1);
+      mbar_init(&S.vempty[s], 2);
     }
     for (int i = 0; i < kRwItems; ++i) {
       mbar_init(&S.ifull[i], 1);
-      mbar_init(&S.iempty[i], 8 + 1);  // softmax warps, the issuer
+      mbar_init(&S.iempty[i], 8 + 1 + 1);  // softmax warps, the issuer, the V producer
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.qfull[i], 1);
@@ -555,44 +605,19 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           if (lane == 0) mbar_arrive(&S.ifull[slot]);
           return true;
         };
-        // one box a lane: its page and half of the tile (paged), or its half
-        const int psz = kSrc == kSrcPaged ? min(p.page_size, 128) : 128;
-        const int boxes = (128 / psz) * kHalves, box_page = lane / kHalves, box_half = lane % kHalves;
         ok = publish(0);
         while (ok) {
           const RowItem& it = S.item[K & (kRwItems - 1)];
           if (it.stop) break;
-          const int c0 = it.tile0, c1 = it.tile0 + it.ntile, k1 = it.k1, ih = it.h, ib = it.b;
-          const int key_row0 = it.key_row0, q_row = it.row0, q_step = it.alt ? 0 : tpt;
-          auto page_of = [&](int tile) -> int {
-            if constexpr (kSrc == kSrcPaged) {
-              const int key = tile * 128 + box_page * psz;
-              if (lane < boxes && key < k1) {
-                const int id = p.block_table[static_cast<int64_t>(ib) * p.pages_per_seq + key / p.page_size];
-                if (id >= 0 && id < p.num_pages) return id;
-                atomicOr(&p.hdr->status, FD_FLAG_BAD_PAGE);
-              }
-              return p.num_pages;  // outside the map: the copy writes zeros
-            }
-            return 0;
-          };
-          auto load = [&](const CUtensorMap* map, uint32_t c, int tile, int page) -> bool {
-            const int st = c % kStages;
-            if (!row_wait(&S.empty[st], ((c / kStages) & 1u) ^ 1u, &S.abort_flag)) return false;
-            if (lane == 0) mbar_arrive_expect_tx(&S.full[st], kHalves * 128u * static_cast<uint32_t>(p.kv_box_rows * (128 / psz)));
-            __syncwarp();
-            if (lane < boxes) {
-              __nv_bfloat16* dst = S.kv[st][box_half] + box_page * psz * 64;
-              if constexpr (kSrc == kSrcPacked) tma_load_3d(dst, map, &S.full[st], 64 * box_half, ih, key_row0 + tile * 128);
-              else if constexpr (kSrc == kSrcCache) tma_load_4d(dst, map, &S.full[st], 64 * box_half, tile * 128, ih, ib);
-              else tma_load_4d(dst, map, &S.full[st], 64 * box_half, tile * 128 % p.page_size, ih, page);
-            }
-            return true;
-          };
-          int page = page_of(c0);
+          const int c0 = it.tile0, c1 = it.tile0 + it.ntile, ih = it.h;
+          const int q_row = it.row0, q_step = it.alt ? 0 : tpt;
+          const KeyBoxes<kD, kSrc> box(p, it, lane);
+          int page = box.page(p, c0);
 #pragma unroll 1
           for (int j = c0; j < c1; ++j, ++T) {
-            if (!load(&tmap_k, 2 * T, j, page)) { ok = false; break; }
+            const int st = T % kKStages;
+            if (!row_wait(&S.kempty[st], ((T / kKStages) & 1u) ^ 1u, &S.abort_flag)) { ok = false; break; }
+            box.load(p, &tmap_k, &S.kfull[st], S.k[st][0], j, page);
             if (j == c0) {
 #pragma unroll 1
               for (int L = 0; L < 2; ++L) {
@@ -603,8 +628,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
               }
               if (!ok) break;
             }
-            if (!load(&tmap_v, 2 * T + 1, j, page)) { ok = false; break; }
-            if (j + 1 < c1) page = page_of(j + 1);
+            if (j + 1 < c1) page = box.page(p, j + 1);
             // the ring holds two tiles: plan while they are worked on
             if (j == min(c0 + 1, c1 - 1) && !(ok = publish(K + 1))) break;
           }
@@ -618,80 +642,72 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       }
       __syncwarp();
       if (S.abort_flag && lane == 0) {  // copies still in flight land before the CTA leaves
-        for (uint32_t back = 1; back <= kStages + 1u && back <= 2 * T + 1; ++back) {
-          const uint32_t c = 2 * T + 1 - back;
-          (void)row_poll(&S.full[c % kStages], (c / kStages) & 1u);
-        }
+        for (uint32_t back = 1; back <= kKStages && back <= T; ++back) (void)row_poll(&S.kfull[(T - back) % kKStages], ((T - back) / kKStages) & 1u);
         for (int L = 0; L < 2; ++L) {
           if (K > 0) (void)row_poll(&S.qfull[L], (K - 1) & 1u);
           (void)row_poll(&S.qfull[L], K & 1u);
         }
       }
+    } else if (warp == kRwVProducer) {
+      // ======================= TMA of V =======================
+      // A warp of its own: V's stages are held through the softmax, and K must not queue behind them.
+      uint32_t T = 0;
+      bool ok = true;
+      for (uint32_t K = 0; ok; ++K) {
+        const int slot = K & (kRwItems - 1);
+        if (!row_wait(&S.ifull[slot], (K / kRwItems) & 1u, &S.abort_flag)) break;
+        const RowItem& it = S.item[slot];
+        if (it.stop) break;
+        const int c0 = it.tile0, c1 = it.tile0 + it.ntile;
+        const KeyBoxes<kD, kSrc> box(p, it, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.iempty[slot]);
+        int page = box.page(p, c0);
+#pragma unroll 1
+        for (int j = c0; j < c1; ++j, ++T) {
+          const int st = T % kVStages;
+          if (!row_wait(&S.vempty[st], ((T / kVStages) & 1u) ^ 1u, &S.abort_flag)) { ok = false; break; }
+          box.load(p, &tmap_v, &S.vfull[st], S.v[st][0], j, page);
+          if (j + 1 < c1) page = box.page(p, j + 1);
+        }
+      }
+      if (S.abort_flag && lane == 0)
+        for (uint32_t back = 1; back <= kVStages && back <= T; ++back) (void)row_poll(&S.vfull[(T - back) % kVStages], ((T - back) / kVStages) & 1u);
     } else if (warp == kRwIssue) {
       // ======================= tensor-core issue =======================
-      // Step T of the key tiles: for each lane that uses tile T the product P·V of the lane's previous
-      // tile, then the scores of tile T over the same columns (products of one thread run in the
-      // order of their issue). The lanes' pairs of products alternate, so that one lane's softmax
-      // runs beside the other lane's products: with a thread a lane the commits queued behind the
-      // other lane's products, both softmaxes ran at once and a tile took 4830 cycles.
+      // Of a two-tile item, tile by tile and lane by lane: P·V of tile i - 1, then the scores of tile i over
+      // the P just read (products of one thread run in the order of their issue). The lanes' products
+      // alternate, so that one lane's softmax runs beside the other's products: with a thread a lane the
+      // commits queued behind the other lane's products, both softmaxes ran at once, and a tile took 4830
+      // cycles. Scores ahead of P·V did not pay: D 128 has the columns for half a tile only, and a 128 x 64
+      // product costs the tensor pipe as much as a 128 x 128 one (849 instead of 1098 TFLOP/s at 16384);
+      // with D 64, which has them for a whole tile, 602 instead of 644 TFLOP/s at 8192. An item of one row
+      // tile has its lanes on alternate key tiles.
       const uint32_t idesc_s = idesc_bf16_f32(128, 128, false, false);
       const uint32_t idesc_o = idesc_bf16_f32(128, kD, false, true);
       const uint64_t q_desc = smem_desc(smem_u32(S.q[0][0]), 16, 1024, kLayoutSW128);
-      const uint64_t k_desc = smem_desc(smem_u32(S.kv[0][0]), 16, 1024, kLayoutSW128);
-      const uint64_t v_desc = smem_desc(smem_u32(S.kv[0][0]), kRwHalf, 1024, kLayoutSW128);
-      constexpr uint32_t kStageDesc = kHalves * (kRwHalf >> 4);  // a stage in the start-address field
+      const uint64_t k_desc = smem_desc(smem_u32(S.k[0][0]), 16, 1024, kLayoutSW128);
+      const uint64_t v_desc = smem_desc(smem_u32(S.v[0][0]), kRwHalf, 1024, kLayoutSW128);
+      constexpr uint32_t kTileDesc = kHalves * (kRwHalf >> 4);  // 128 rows in the start-address field
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       // A lane's state (both lanes' stay in registers: every use names its lane at compile time).
       struct Turn {
-        uint32_t pend = 0;      // 1 + the tile count T of the scores whose product is still to issue
-        uint32_t steps = 0;     // its key steps of 16
-        uint32_t J = 0;         // tiles of the lane so far
+        uint32_t pend = 0;        // 1 + the tile count T of the tile whose product is still to issue
+        uint32_t steps = 0;       // its key steps of 16
+        uint32_t J = 0;           // tiles of the lane started
         int first = 0, last = 0;  // the pending tile is its item's first (2 + a parity) / last
         bool alone = false;       // the other lane does not use it
-        int i = 0, used = 0, next = 0, step = 1, kend = 0;  // this item: tiles done, all, the next one
+        int i = 0, used = 0, kend = 0;  // this item: tiles done, all, the end of the lane's keys
       } st0, st1;
-      uint32_t T = 0;
+      uint32_t T = 0;  // tiles of the items before
       bool ok = true;
-      auto product = [&](auto lane_no, Turn& st) -> bool {  // P·V of the lane's pending tile
+      // the scores of tile count t into the lane's columns
+      auto scores = [&](auto lane_no, uint32_t t) -> bool {
         constexpr int L = decltype(lane_no)::value;
-        const uint32_t cv = 2 * (st.pend - 1) + 1, sv = cv % kStages;
-        st.pend = 0;
-        if (!row_wait_warp(&S.full[sv], (cv / kStages) & 1u, &S.abort_flag)) return false;
-        if (st.first != 0 && !row_wait_warp(&S.oempty[L], st.first & 1u, &S.abort_flag)) return false;
-        const uint32_t s_col = tm + 128 * L, o_col = tm + kRwColO + kD * L;
-        const uint64_t vd = v_desc + static_cast<uint64_t>(sv * kStageDesc);
-        const uint32_t acc = st.first != 0 ? 0u : 1u;
-#pragma unroll 1
-        for (uint32_t half = 0; half < 2; ++half) {
-          if (!row_wait_warp(&S.pfull[L][half], (st.J - 1) & 1u, &S.abort_flag)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (uint32_t i = 0; i < 4; ++i) {
-              const uint32_t kk = 4 * half + i;
-              if (kk < st.steps) umma_bf16_ts(o_col, s_col + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, kk > 0 ? 1u : acc);
-            }
-          }
-          __syncwarp();
-        }
-        if (elect_one()) {
-          umma_commit(&S.empty[sv]);
-          if (st.alone) umma_commit(&S.empty[sv]);
-          if (st.last != 0) umma_commit(&S.ofin[L]);
-        }
-        __syncwarp();
-        return true;
-      };
-      auto turn = [&](auto lane_no, Turn& st, uint32_t K, int j, bool use, bool other) -> bool {
-        constexpr int L = decltype(lane_no)::value;
-        // an unused tile: only a product two tiles back, whose stage the next V tile needs
-        if (!use) return st.pend == 0 || st.pend + 1 > T || product(lane_no, st);
-        if (st.pend != 0 && !product(lane_no, st)) return false;
-        const uint32_t ck = 2 * T, sk = ck % kStages;
-        if (!row_wait_warp(&S.full[sk], (ck / kStages) & 1u, &S.abort_flag)) return false;
-        if (st.i == 0 && !row_wait_warp(&S.qfull[L], K & 1u, &S.abort_flag)) return false;
+        const uint32_t st = t % kKStages;
+        if (!row_wait_warp(&S.kfull[st], (t / kKStages) & 1u, &S.abort_flag)) return false;
         tc_fence_after();
-        const uint64_t qd = q_desc + static_cast<uint64_t>(L * kStageDesc), kd = k_desc + static_cast<uint64_t>(sk * kStageDesc);
+        const uint64_t qd = q_desc + static_cast<uint64_t>(L * kTileDesc), kd = k_desc + static_cast<uint64_t>(st * kTileDesc);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
@@ -701,21 +717,60 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           umma_commit(&S.sfull[L]);  // the softmax gives K's stage back
         }
         __syncwarp();
-        st.pend = T + 1;
+        return true;
+      };
+      auto product = [&](auto lane_no, Turn& st) -> bool {  // P·V of the lane's pending tile
+        constexpr int L = decltype(lane_no)::value;
+        const uint32_t t = st.pend - 1, sv = t % kVStages;
+        st.pend = 0;
+        if (!row_wait_warp(&S.vfull[sv], (t / kVStages) & 1u, &S.abort_flag)) return false;
+        if (st.first != 0 && !row_wait_warp(&S.oempty[L], st.first & 1u, &S.abort_flag)) return false;
+        const uint32_t s_col = tm + 128 * L, o_col = tm + kRwColO + kD * L;
+        const uint64_t vd = v_desc + static_cast<uint64_t>(sv * kTileDesc);
+        const uint32_t acc = st.first != 0 ? 0u : 1u;
+#pragma unroll
+        for (uint32_t half = 0; half < 2; ++half) {
+          if (!row_wait_warp(&S.pfull[L][half], (st.J - 1) & 1u, &S.abort_flag)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (uint32_t kk = 4 * half; kk < 4 * half + 4; ++kk)
+              if (kk < st.steps) umma_bf16_ts(o_col, s_col + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, kk > 0 ? 1u : acc);
+          }
+        }
+        if (elect_one()) {
+          umma_commit(&S.vempty[sv]);
+          if (st.alone) umma_commit(&S.vempty[sv]);
+          if (st.last != 0) umma_commit(&S.ofin[L]);
+        }
+        __syncwarp();
+        return true;
+      };
+      // the lane's next tile of this item, count t, whose scores are issued
+      auto started = [&](auto lane_no, Turn& st, uint32_t K, uint32_t t, int tile, bool alone) {
+        constexpr int L = decltype(lane_no)::value;
+        st.pend = t + 1;
         // key steps of 16 up to the lane's last visible key
-        st.steps = static_cast<uint32_t>(min(128, st.kend - j * 128) + 15) >> 4;
+        st.steps = static_cast<uint32_t>(min(128, st.kend - tile * 128) + 15) >> 4;
         st.first = st.i == 0 ? 2 + static_cast<int>((K & 1u) ^ 1u) : 0;
         st.last = ++st.i == st.used;
-        st.alone = !other;
+        st.alone = alone;
         if (st.last != 0 && elect_one()) umma_commit(&S.qempty[L]);
-        st.next += st.step;
+        __syncwarp();
         ++st.J;
+      };
+      // a tile of the lane, after the product that is still to issue
+      auto begin = [&](auto lane_no, Turn& st, uint32_t K, uint32_t t, int tile, bool alone) -> bool {
+        constexpr int L = decltype(lane_no)::value;
+        if (st.i == 0 && !row_wait_warp(&S.qfull[L], K & 1u, &S.abort_flag)) return false;
+        if (st.pend != 0 && !product(lane_no, st)) return false;
+        if (!scores(lane_no, t)) return false;
+        started(lane_no, st, K, t, tile, alone);
         return true;
       };
       // an item that gives the lane nothing to do: its Q goes back unread, its (empty) O is there
       auto skip = [&](auto lane_no, Turn& st, uint32_t K) -> bool {
         constexpr int L = decltype(lane_no)::value;
-        if (st.used != 0) return true;
         if (!row_wait_warp(&S.qfull[L], K & 1u, &S.abort_flag)) return false;
         if (lane == 0) mbar_arrive(&S.qempty[L]);
         if (st.pend != 0 && !product(lane_no, st)) return false;
@@ -732,88 +787,85 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         const auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
         if (uniform(it.stop)) break;
         const int ntile = uniform(it.ntile), alt = uniform(it.alt);
-        auto begin = [&](int L, Turn& st) {
-          st.i = 0;
-          st.used = uniform(it.used[L]);
-          st.next = alt ? L : 0;
-          st.step = alt ? 2 : 1;
-          st.kend = uniform(it.kend[L]);
-        };
-        begin(0, st0);
-        begin(1, st1);
+        st0.i = st1.i = 0;
+        st0.used = uniform(it.used[0]);
+        st1.used = uniform(it.used[1]);
+        st0.kend = uniform(it.kend[0]);
+        st1.kend = uniform(it.kend[1]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.iempty[slot]);
-        // Tiles [1, used) of a two-tile item, which both lanes use: the products of the tile before are
-        // whole. The general turns below cost the issuing warp ~600 cycles of bookkeeping each, which
-        // leaves the tensor pipe idle as long.
-        const int plain = st0.step == 1 ? st0.used : 0;
-        for (int j = 0; ok && j < ntile; ++j, ++T) {
-          if (j == 1 && plain > 1) {
-            uint32_t sk = 2 * T % kStages, pk = (2 * T / kStages) & 1u;          // K of tile T
-            uint32_t sv = (2 * T - 1) % kStages, pv = ((2 * T - 1) / kStages) & 1u;  // V of tile T - 1
-            uint32_t p0 = (st0.J - 1) & 1u, p1 = (st1.J - 1) & 1u;
-            const uint32_t po = (K & 1u) ^ 1u;
-            auto lane_turn = [&](auto lane_no, uint32_t parity, uint32_t acc, uint64_t kd, uint64_t vd, bool last) -> bool {
+        if (alt) {
+#pragma unroll 1
+          for (int j = 0; ok && j < ntile; ++j)
+            ok = (j & 1) == 0 ? begin(lane0, st0, K, T + j, j, true) : begin(lane1, st1, K, T + j, j, true);
+          if (ok && st1.used == 0) ok = skip(lane1, st1, K);
+        } else {
+          // lane 1 uses every tile, lane 0 all but the last or all
+          const int n0 = st0.used;
+          if (n0 > 0) ok = begin(lane0, st0, K, T, 0, false);
+          ok = ok && begin(lane1, st1, K, T, 0, n0 == 0);
+          if (ok && n0 == 0) ok = skip(lane0, st0, K);
+          // Tiles that both lanes use: whole products of the tile before. Kept lean: with the bookkeeping
+          // of begin() in this loop the issuing warp, not the tensor pipe, set the pace (976 instead of
+          // 1073 TFLOP/s at 4096).
+          const uint32_t first = (K & 1u) ^ 1u;
+#pragma unroll 1
+          for (int j = 1; ok && j < n0; ++j) {
+            const uint32_t tv = T + j - 1, ts = T + j;
+            const uint32_t sv = tv % kVStages, sk = ts % kKStages;
+            ok = row_wait_warp(&S.vfull[sv], (tv / kVStages) & 1u, &S.abort_flag) &&
+                 row_wait_warp(&S.kfull[sk], (ts / kKStages) & 1u, &S.abort_flag);
+            if (j == 1)
+              ok = ok && row_wait_warp(&S.oempty[0], first, &S.abort_flag) && row_wait_warp(&S.oempty[1], first, &S.abort_flag);
+            if (!ok) break;
+            const uint64_t vd = v_desc + static_cast<uint64_t>(sv * kTileDesc), kd = k_desc + static_cast<uint64_t>(sk * kTileDesc);
+            const uint32_t acc = j > 1 ? 1u : 0u;
+            auto lean = [&](auto lane_no, Turn& st, bool last) -> bool {
               constexpr int L = decltype(lane_no)::value;
+              const uint32_t s_col = tm + 128 * L, o_col = tm + kRwColO + kD * L, parity = (st.J - 1) & 1u;
               if (!row_wait_warp(&S.pfull[L][0], parity, &S.abort_flag)) return false;
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  umma_bf16_ts(tm + kRwColO + kD * L, tm + 128 * L + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, kk > 0 ? 1u : acc);
+                  umma_bf16_ts(o_col, s_col + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, kk > 0 ? 1u : acc);
               }
               if (!row_wait_warp(&S.pfull[L][1], parity, &S.abort_flag)) return false;
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
                 for (int kk = 4; kk < 8; ++kk)
-                  umma_bf16_ts(tm + kRwColO + kD * L, tm + 128 * L + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
-                umma_commit(&S.empty[sv]);
+                  umma_bf16_ts(o_col, s_col + 8 * kk, vd + static_cast<uint64_t>(kk * 128), idesc_o, 1u);
+                umma_commit(&S.vempty[sv]);
 #pragma unroll
                 for (int kk = 0; kk < kD / 16; ++kk) {
                   const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kRwHalf >> 4) + (kk & 3) * 2);
-                  umma_bf16_ss(tm + 128 * L, q_desc + L * kStageDesc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
+                  umma_bf16_ss(s_col, q_desc + L * kTileDesc + off, kd + off, idesc_s, kk > 0 ? 1u : 0u);
                 }
                 umma_commit(&S.sfull[L]);
                 if (last) umma_commit(&S.qempty[L]);
               }
+              ++st.J;
               __syncwarp();
               return true;
             };
-            const int n = plain - 1;
-            for (int i = 0; i < n; ++i) {
-              const uint64_t kd = k_desc + static_cast<uint64_t>(sk * kStageDesc), vd = v_desc + static_cast<uint64_t>(sv * kStageDesc);
-              ok = row_wait_warp(&S.full[sv], pv, &S.abort_flag) && row_wait_warp(&S.full[sk], pk, &S.abort_flag);
-              if (i == 0) ok = ok && row_wait_warp(&S.oempty[0], po, &S.abort_flag) && row_wait_warp(&S.oempty[1], po, &S.abort_flag);
-              const uint32_t acc = i > 0 ? 1u : 0u;
-              ok = ok && lane_turn(lane0, p0, acc, kd, vd, i == n - 1) && lane_turn(lane1, p1, acc, kd, vd, i == n - 1 && st1.used == plain);
-              if (!ok) break;
-              if ((sk += 2) >= kStages) { sk -= kStages; pk ^= 1u; }
-              if ((sv += 2) >= kStages) { sv -= kStages; pv ^= 1u; }
-              p0 ^= 1u;
-              p1 ^= 1u;
-            }
-            if (!ok) break;
-            j += n;
-            T += n;
+            ok = lean(lane0, st0, j == n0 - 1) && lean(lane1, st1, j == ntile - 1);
+          }
+          if (n0 > 1) {
             auto forward = [&](Turn& st) {
-              st.pend = T;
-              st.steps = static_cast<uint32_t>(min(128, st.kend - (j - 1) * 128) + 15) >> 4;
+              st.pend = T + n0;
+              st.steps = static_cast<uint32_t>(min(128, st.kend - (n0 - 1) * 128) + 15) >> 4;
               st.first = 0;
               st.alone = false;
-              st.i += n;
-              st.last = st.i == st.used;
-              st.next += n;
-              st.J += n;
+              st.i = n0;
+              st.last = n0 == st.used;
             };
             forward(st0);
             forward(st1);
-            if (j >= ntile) break;
           }
-          const bool use0 = st0.i < st0.used && j == st0.next, use1 = st1.i < st1.used && j == st1.next;
-          ok = turn(lane0, st0, K, j, use0, use1) && turn(lane1, st1, K, j, use1, use0);
+          if (ok && ntile > n0 && ntile > 1) ok = begin(lane1, st1, K, T + ntile - 1, ntile - 1, true);  // lane 1's last
         }
-        ok = ok && skip(lane0, st0, K) && skip(lane1, st1, K);
+        T += ntile;
       }
       if (ok && st0.pend != 0) ok = product(lane0, st0);
       if (ok && st1.pend != 0) ok = product(lane1, st1);
@@ -848,6 +900,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       for (int a = 0; a < 4; ++a) sum2[a] = 0;
       for (int i = 0; i < used; ++i, ++J) {
         const int j = alt ? 2 * i + L : i, tile = it.tile0 + j;
+        const uint32_t t = T + j;
         uint32_t w[4];
         // tiles that every row of this warp sees whole need no mask
         bool full;
@@ -856,8 +909,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         if (!full) visible_words<kCausal>(p, it, tile, pos, row_ok, static_cast<int64_t>(it.row0) + pos, w);
         if (!row_wait(&S.sfull[L], J & 1u, &S.abort_flag)) { ok = false; break; }
         tc_fence_after();
-        // K of this tile is no longer read (its stage expects two arrivals; a tile of one lane gives both)
-        if (warp == 4 * L && lane == 0) mbar_arrive_n(&S.empty[2 * (T + j) % kStages], i < both ? 1u : 2u);
+        // K is no longer read (its stage expects two arrivals; a tile of one lane gives both)
+        if (warp == 4 * L && lane == 0) mbar_arrive_n(&S.kempty[t % kKStages], i < both ? 1u : 2u);
         if (!full) {
           // in tensor memory, so that the scores below come straight from there in every tile
 #pragma unroll 1
@@ -875,12 +928,11 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         const int valid = it.k1 - tile * 128;
         if (valid < 128 && (valid & 15) != 0) {
           // zero V rows [valid, next multiple of 16): they may lie behind the request's keys
-          const uint32_t cv = 2 * (T + j) + 1;
-          if (!row_wait(&S.full[cv % kStages], (cv / kStages) & 1u, &S.abort_flag)) { ok = false; break; }
+          if (!row_wait(&S.vfull[t % kVStages], (t / kVStages) & 1u, &S.abort_flag)) { ok = false; break; }
           const int r0 = valid, nr = ((valid + 15) & ~15) - r0;
           for (int c = r; c < nr * 8 * kHalves; c += 128) {
             const int row = r0 + c / (8 * kHalves);
-            *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(S.kv[cv % kStages][(c / 8) % kHalves]) + row * 128 +
+            *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(S.v[t % kVStages][(c / 8) % kHalves]) + row * 128 +
                                       (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
@@ -889,38 +941,30 @@ __global__ void __launch_bounds__(kRwThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * c));
         tmem_wait_ld();
-        // P of keys 32 c + [0, 32), from the maximum m; their sums into add2
+        // weights 2^(score - m) of 64 scores as bf16 pairs, their sums into add2. -m: 0 where every score is
+        // -inf so far, NaN for a row that saw +inf (as for one that saw NaN)
         uint64_t add2[4];
-        auto weights = [&](int c, uint64_t negm2) {
-          uint32_t out[16];
+        auto weights = [&](int half, uint32_t (&out)[32]) {
+          const float n = m == -INFINITY ? 0.f : fmaf(m, 0.f, -m);
+          const uint64_t negm2 = pair_f32(n, n);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const uint64_t a = fma_f32x2(pair_f32(__uint_as_float(x[32 * c + e]), __uint_as_float(x[32 * c + e + 1])), scale2, negm2);
+          for (int e = 0; e < 64; e += 2) {
             float a0, a1;
-            unpair_f32(a, a0, a1);
+            unpair_f32(fma_f32x2(pair_f32(__uint_as_float(x[64 * half + e]), __uint_as_float(x[64 * half + e + 1])), scale2, negm2), a0, a1);
             a0 = fast_exp2(a0);
             a1 = fast_exp2(a1);
             out[e >> 1] = pack_bf16(a0, a1);
             add2[(e >> 1) & 3] = add_f32x2(add2[(e >> 1) & 3], pair_f32(a0, a1));
           }
-          tmem_st16(s_col + 16 * c, out);
-        };
-        // -m; 0 where every score is -inf so far, NaN for a row that saw +inf (as for one that saw NaN)
-        auto minus = [&]() {
-          const float n = m == -INFINITY ? 0.f : fmaf(m, 0.f, -m);
-          return pair_f32(n, n);
         };
         // The first half of the tile is weighted with the maximum so far while the whole tile's maximum
         // is found beside it; only where that has grown by more than 2^8 is it weighted again.
+        uint32_t out[32];
         bool checked = false;
         for (;;) {
 #pragma unroll
           for (int a = 0; a < 4; ++a) add2[a] = 0;
-          if (i > 0 || checked) {
-            const uint64_t negm2 = minus();
-            weights(0, negm2);
-            weights(1, negm2);
-          }
+          if (i > 0 || checked) weights(0, out);
           if (checked) break;
           checked = true;
           float mx[4];
@@ -937,7 +981,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           const float alpha = move ? (m == -INFINITY ? 0.f : fast_exp2(m - mn)) : 1.f;
           if (move) m = mn;
           if (i > 0) {
-            // the scores of this tile were issued after the last product into O had completed
+            // the scores of this tile were issued after the last product into O, and are there
 #pragma unroll 1
             for (int c = 0; c < kD; c += 16) {
               uint32_t o[16];
@@ -952,13 +996,13 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             for (int a = 0; a < 4; ++a) sum2[a] = fma_f32x2(sum2[a], alpha2, 0ull);
           }
         }
+        tmem_st32(s_col, out);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.pfull[L][0]);
-        const uint64_t negm2 = minus();
-        weights(2, negm2);
-        weights(3, negm2);
+        weights(1, out);
+        tmem_st32(s_col + 32, out);
 #pragma unroll
         for (int a = 0; a < 4; ++a) sum2[a] = add_f32x2(sum2[a], add2[a]);
         tmem_wait_st();
