@@ -40,42 +40,61 @@ FD_HD int32_t rows_item_keys(bool causal, int32_t tpt, int32_t n, int32_t keys, 
 
 // CTAs that take part: as many as there are items, or as there are stretches of kMinPiece tiles.
 FD_HD int32_t rows_active(int64_t weight, int64_t items, int32_t nctas) {
-  const int64_t n = weight / (kMinPiece * 128);
+  const int64_t n = weight / (kMinPiece * 128);  // a shift
   const int64_t m = items > n ? items : n;
   return m < nctas ? (m < 1 ? 1 : static_cast<int32_t>(m)) : nctas;
 }
 
-// Where CTA i's stretch begins.
-FD_HD int64_t rows_bound(int64_t weight, int32_t nact, int32_t i) {
-  return weight / nact * i + weight % nact * i / nact;
+// The line cut into stretches, of `share` units each and one more in the first `rest`. Dividing 64-bit
+// integers is a subroutine of ~100 dependent instructions, and a CTA looks at some twenty bounds before
+// its first load: one division here, in doubles, none below.
+struct RowsLine {
+  int64_t share;
+  int32_t rest, nact;
+};
+FD_HD int64_t rows_quotient(int64_t x, int64_t d) {  // floor(x / d), x >= 0, d > 0
+  int64_t q = static_cast<int64_t>(static_cast<double>(x) / static_cast<double>(d));
+  while (q * d > x) --q;
+  while ((q + 1) * d <= x) ++q;
+  return q;
 }
+FD_HD RowsLine rows_line(int64_t weight, int32_t nact) {
+  RowsLine n;
+  n.share = rows_quotient(weight, nact);
+  n.rest = static_cast<int32_t>(weight - n.share * nact);
+  n.nact = nact;
+  return n;
+}
+// Where CTA i's stretch begins (i = nact: the line's end).
+FD_HD int64_t rows_bound(const RowsLine& n, int32_t i) { return n.share * i + (i < n.rest ? i : n.rest); }
 
-// The key tile at which the point x of the line cuts an item of `tiles` key tiles at [a, a + w).
+// The key tile at which the point x of the line cuts an item of `tiles` key tiles at [a, a + w). In fp32:
+// every CTA finds the same tile, and each rounding keeps the order of two points.
 FD_HD int32_t rows_cut(int64_t x, int64_t a, int64_t w, int32_t tiles) {
   if (x <= a) return 0;
   if (x >= a + w) return tiles;
-  const int32_t t = static_cast<int32_t>(tiles * (x - a) / w);
+  const float part = static_cast<float>(static_cast<uint32_t>(x - a)) / static_cast<float>(static_cast<uint32_t>(w));
+  const int32_t t = static_cast<int32_t>(part * static_cast<float>(tiles));
   if (t < kMinPiece) return 0;
   return tiles - t < kMinPiece ? tiles : t;
 }
 
 // The cuts of an item: bounds first .. first + count - 1 cut it (count 0: one CTA has all of it).
 // Bounds that lie inside the item without cutting it stand at its ends, a few at most.
-FD_HD void rows_cuts(int64_t weight, int32_t nact, int64_t a, int64_t w, int32_t tiles, int32_t cta,
-                     int32_t* first, int32_t* count) {
+FD_HD void rows_cuts(const RowsLine& n, int64_t a, int64_t w, int32_t tiles, int32_t cta, int32_t* first, int32_t* count) {
   int32_t lo = cta, hi = cta;  // a bound in or at the item: the caller's own stretch meets the item
-  while (lo > 0 && rows_cut(rows_bound(weight, nact, lo), a, w, tiles) > 0) {
+  while (lo > 0 && rows_cut(rows_bound(n, lo), a, w, tiles) > 0) {
     // step down in strides as long as the bound stays inside
     int32_t step = 1;
-    while (lo - 2 * step > 0 && rows_cut(rows_bound(weight, nact, lo - 2 * step), a, w, tiles) > 0) step *= 2;
+    while (lo - 2 * step > 0 && rows_cut(rows_bound(n, lo - 2 * step), a, w, tiles) > 0) step *= 2;
     lo -= step;
   }
   ++lo;
-  while (rows_cut(rows_bound(weight, nact, lo), a, w, tiles) == 0) ++lo;  // bounds snapped to the start
+  while (rows_cut(rows_bound(n, lo), a, w, tiles) == 0) ++lo;  // bounds snapped to the start
   if (hi < lo) hi = lo;
-  while (hi < nact && rows_cut(rows_bound(weight, nact, hi), a, w, tiles) < tiles) {
+  while (hi < n.nact && rows_cut(rows_bound(n, hi), a, w, tiles) < tiles) {
     int32_t step = 1;
-    while (hi + 2 * step < nact && rows_cut(rows_bound(weight, nact, hi + 2 * step), a, w, tiles) < tiles) step *= 2;
+    while (hi + 2 * step < n.nact && rows_cut(rows_bound(n, hi + 2 * step), a, w, tiles) < tiles) step *= 2;
     hi += step;
   }
   *first = lo;

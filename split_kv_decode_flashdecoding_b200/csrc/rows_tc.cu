@@ -52,7 +52,7 @@ enum RowSource { kSrcPacked = 0, kSrcCache = 1, kSrcPaged = 2 };
 struct RowItem {
   int32_t stop;
   int32_t b, h;             // request, KV head
-  int32_t row0, t0, nt;     // packed row of the first token; its index in the request; tokens
+  int32_t row0, t0;         // packed row of the first token; its index in the request
   int32_t key_row0;         // prompt: packed row of the request's first key
   int32_t tile0, ntile;     // key tiles [tile0, tile0 + ntile)
   int32_t k1;               // keys of the item (all pieces): tiles hold keys < k1
@@ -61,7 +61,8 @@ struct RowItem {
   // by lane: its tokens, the key tiles it uses, the end of its visible keys from tile0's first key on.
   // The i-th tile of lane L is tile0 + i, or tile0 + 2 i + L (alt).
   int32_t tokens[2], used[2], kend[2];
-  int32_t cut0, cuts, piece;  // rows_cuts of a cut item (cuts 0: whole), this piece's index
+  int32_t whole;              // this CTA has all its key tiles; if not, when cfull has arrived:
+  int32_t cut0, cuts, piece;  // rows_cuts of the item, this piece's index
 };
 
 template <int kD>
@@ -73,16 +74,17 @@ struct __align__(1024) RwSmem {
   __nv_bfloat16 k[kKStages][kHalves][128 * 64];
   __nv_bfloat16 v[kVStages][kHalves][128 * 64];
   RowItem item[kRwItems];
+  int32_t req[kRwThreads][3];  // a thread's first request: rows, keys, prefix
   float2 xend[8][32];  // softmax warps: a row's (m, l) at the end of an alt item, for the other lane's warp
   union {
-    struct {  // plan: work, rows and items of a thread's requests
-      int64_t part_w[kRwThreads];
-      int32_t part_r[kRwThreads], part_i[kRwThreads];
+    struct {  // plan: work and rows of a thread's requests; work, rows and items of a warp's
+      int64_t part_w[kRwThreads], warp_w[kRwThreads / 32];
+      int32_t part_r[kRwThreads], warp_r[kRwThreads / 32], warp_i[kRwThreads / 32];
     };
     uint4 stage[8][128];  // output: a warp's rows, 32 columns
   };
   uint64_t kfull[kKStages], kempty[kKStages], vfull[kVStages], vempty[kVStages];
-  uint64_t qfull[2], qempty[2], ifull[kRwItems], iempty[kRwItems];
+  uint64_t qfull[2], qempty[2], ifull[kRwItems], cfull[kRwItems], iempty[kRwItems];
   // by lane: a tile's scores are there, P of keys [0, 64) and of [64, 128) is stored, O is complete, is read
   uint64_t sfull[2], pfull[2][2], ofin[2], oempty[2];
   uint64_t xpair[4];  // exchanges of the two lanes' warps of a row quarter (alt items)
@@ -166,8 +168,29 @@ __device__ __forceinline__ bool row_wait_warp(uint64_t* bar, uint32_t parity, vo
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, row_wait(bar, parity, abort_flag));
 }
+// Sum over a warp; running sums of its lanes.
+__device__ __forceinline__ int64_t warp_sum(int64_t x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ void warp_scan(int64_t& x, int64_t& y, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
+    if (lane >= o) { x += a; y += b; }
+  }
+}
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+// Counts this warp's stores (after a __syncwarp) as there, and makes those counted before visible to a warp
+// that passes its next __syncwarp.
+__device__ __forceinline__ uint32_t atomic_add_acq_rel(uint32_t* at, uint32_t n) {
+  uint32_t r;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], %2;" : "=r"(r) : "l"(at), "r"(n) : "memory");
+  return r;
 }
 
 // n low bits set (n <= 0: none, n >= 32: all).
@@ -249,12 +272,13 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
           l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   };
   auto over = [](float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); };  // 0 for an empty row; NaN stays
+  const bool live = (((quad * 32 + lane) * p.g_recip16) >> 16) < it.tokens[t];  // this thread's row
   // pieces: O as [slot][row tile][D / 4][128 rows] float4, (m, l) as [slot][warp][32 rows] float2
   ulonglong2* part_o = reinterpret_cast<ulonglong2*>(p.part_o) + quad * 32 + lane;
   float2* part_ml = reinterpret_cast<float2*>(p.part_ml) + warp * 32 + lane;
   auto place = [&](int64_t slot, int c) { return ((slot * 2 + t) * (kD / 4) + c / 4) * 128; };
-  const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (it.piece > 0 ? 0 : 1);
-  const bool whole = it.cuts == 0;
+  const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (it.tile0 > 0 ? 0 : 1);  // the first piece: 1
+  const bool whole = it.whole != 0;
   // A lane without tiles has left its accumulator as it was: that one is not looked at.
   const bool none0 = it.used[kAlt ? 0 : t] == 0, none1 = it.used[1] == 0;
   const float scale = whole ? over(l) : 1.f;
@@ -285,7 +309,7 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
     }
     if (whole) {
       emit(c, o);
-    } else {
+    } else if (live) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) part_o[place(part, c) + e * 128] = make_ulonglong2(o[2 * e], o[2 * e + 1]);
     }
@@ -295,24 +319,33 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
     return;
   }
   part_ml[part * 256] = make_float2(m, l);
-  __threadfence();
   __syncwarp();
   uint32_t* counter = &p.hdr->row_pieces[it.cut0][warp >> 2];
   uint32_t before = 0;
-  if (lane == 0) before = (atomicAdd(counter, 1u << (8 * quad)) >> (8 * quad)) & 0xffu;
+  if (lane == 0) before = (atomic_add_acq_rel(counter, 1u << (8 * quad)) >> (8 * quad)) & 0xffu;
   before = __shfl_sync(0xffffffffu, before, 0);
-  if (before != static_cast<uint32_t>(it.cuts)) return;
-  __threadfence();
-  if (lane == 0) atomicSub(counter, static_cast<uint32_t>(it.cuts + 1) << (8 * quad));
-  auto piece_slot = [&](int q) { return 2 * static_cast<int64_t>(it.cut0 - 1 + q) + (q > 0 ? 0 : 1); };
+  __syncwarp();
+  const int cuts = it.cuts, cut0 = it.cut0;
+  if (before != static_cast<uint32_t>(cuts)) return;
+  if (lane == 0) atomicSub(counter, static_cast<uint32_t>(cuts + 1) << (8 * quad));
+  // Four pieces' loads at a time: a load takes ~1000 cycles, and with two in flight the merge of a wide
+  // tree's pieces took 30,000.
+  auto piece_slot = [&](int q) { return 2 * static_cast<int64_t>(cut0 - 1 + q) + (q > 0 ? 0 : 1); };
   float mt = -INFINITY, lt = 0.f;
-  for (int q = 0; q <= it.cuts; ++q) {
-    const float2 ml = __ldcg(part_ml + piece_slot(q) * 256);
-    if (!(ml.y == 0.f)) mt = fmaxf(mt, ml.x);
-  }
-  for (int q = 0; q <= it.cuts; ++q) {
-    const float2 ml = __ldcg(part_ml + piece_slot(q) * 256);
-    if (!(ml.y == 0.f)) lt = fmaf(ml.y, fast_exp2(ml.x - mt), lt);
+#pragma unroll 1
+  for (int q = 0; q <= cuts; q += 4) {
+    float2 ml[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ml[i] = q + i <= cuts ? __ldcg(part_ml + piece_slot(q + i) * 256) : make_float2(-INFINITY, 0.f);
+    float mn = mt;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(ml[i].y == 0.f)) mn = fmaxf(mn, ml[i].x);
+    lt = lt == 0.f ? 0.f : lt * fast_exp2(mt - mn);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!(ml[i].y == 0.f)) lt = fmaf(ml[i].y, fast_exp2(ml[i].x - mn), lt);
+    mt = mn;
   }
   const float total = over(lt);
 #pragma unroll 1
@@ -320,18 +353,27 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
     uint64_t o[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[e] = 0;
-#pragma unroll 2
-    for (int q = 0; q <= it.cuts; ++q) {
-      const float2 ml = __ldcg(part_ml + piece_slot(q) * 256);
-      ulonglong2 y[8];
+#pragma unroll 1
+    for (int q = 0; q <= cuts; q += 4) {
+      float2 ml[4];
+      ulonglong2 y[4][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = __ldcg(part_o + place(piece_slot(q), c) + e * 128);
-      const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - mt) * total;
-      const uint64_t f2 = pair_f32(f, f);
+      for (int i = 0; i < 4; ++i) {
+        const bool there = live && q + i <= cuts;
+        const int64_t slot = piece_slot(q + i);
+        ml[i] = there ? __ldcg(part_ml + slot * 256) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        o[2 * e] = fma_f32x2(y[e].x, f2, o[2 * e]);
-        o[2 * e + 1] = fma_f32x2(y[e].y, f2, o[2 * e + 1]);
+        for (int e = 0; e < 8; ++e) y[i][e] = there ? __ldcg(part_o + place(slot, c) + e * 128) : make_ulonglong2(0ull, 0ull);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = ml[i].y == 0.f ? 0.f : fast_exp2(ml[i].x - mt) * total;
+        const uint64_t f2 = pair_f32(f, f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          o[2 * e] = fma_f32x2(y[i][e].x, f2, o[2 * e]);
+          o[2 * e + 1] = fma_f32x2(y[i][e].y, f2, o[2 * e + 1]);
+        }
       }
     }
     emit(c, o);
@@ -406,6 +448,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     }
     for (int i = 0; i < kRwItems; ++i) {
       mbar_init(&S.ifull[i], 1);
+      mbar_init(&S.cfull[i], 1);
       mbar_init(&S.iempty[i], 8 + 1 + 1);  // softmax warps, the issuer, the V producer
     }
     for (int i = 0; i < 2; ++i) {
@@ -440,13 +483,13 @@ __global__ void __launch_bounds__(kRwThreads, 1)
   const int per = (p.batch + kRwThreads - 1) / kRwThreads;
   auto request = [&](int b, int* n, int* keys, int* prefix) {
     const int len = p.row_lens[b];
+    const int pre = kCausal ? 0 : p.prefix_lens[b];
     *n = max(len, 0);
     *keys = *n;
     *prefix = 0;
     uint32_t flag = len < 0 ? FD_FLAG_LEN_CLAMPED : 0u;
     if constexpr (!kCausal) {
       if (len < 0 || len > 32 * p.mask_words) S.bad = 1;
-      const int pre = p.prefix_lens[b];
       *prefix = clamp_len(pre, p.cap);
       const int64_t end = static_cast<int64_t>(*prefix) + *n;
       *keys = static_cast<int>(min(end, static_cast<int64_t>(p.cap)));
@@ -467,12 +510,29 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       w += p.hkv * rows_weight(kCausal, tpt, keys, pairs);
       rows += n;
       items += pairs;
+      if (i == 0) {
+        S.req[tid][0] = n;
+        S.req[tid][1] = keys;
+        S.req[tid][2] = prefix;
+      }
     }
-    if (rows > p.rows) S.bad = 1;
     if (flag && blockIdx.x == 0) atomicOr(&p.hdr->status, flag);
+    const int32_t r = static_cast<int32_t>(min(rows, static_cast<int64_t>(p.rows) + 1));
     S.part_w[tid] = w;
-    S.part_r[tid] = static_cast<int32_t>(min(rows, static_cast<int64_t>(p.rows) + 1));
-    S.part_i[tid] = items;
+    S.part_r[tid] = r;
+    if (warp * 32 * per < p.batch) {
+      const int64_t warp_w = warp_sum(w), warp_r = warp_sum(static_cast<int64_t>(r));
+      const int32_t warp_i = __reduce_add_sync(0xffffffffu, items);
+      if (warp_r > p.rows) S.bad = 1;
+      if (lane == 0) {
+        S.warp_w[warp] = warp_w;
+        S.warp_r[warp] = static_cast<int32_t>(min(warp_r, static_cast<int64_t>(p.rows)));
+        S.warp_i[warp] = warp_i;
+      }
+    } else if (lane == 0) {
+      S.warp_w[warp] = 0;
+      S.warp_r[warp] = S.warp_i[warp] = 0;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -483,41 +543,34 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     set_regs_less<88>();
     if (warp == kRwProducer) {
       // ======================= plan and TMA =======================
-      // Totals of the threads' stretches, 16 a lane, then this CTA's stretch of the work.
-      int64_t mine_w = 0, mine_r = 0, mine_i = 0;
-      for (int i = 0; i < kRwThreads / 32; ++i) {
-        mine_w += S.part_w[lane * (kRwThreads / 32) + i];
-        mine_r += S.part_r[lane * (kRwThreads / 32) + i];
-        mine_i += S.part_i[lane * (kRwThreads / 32) + i];
-      }
-      int64_t sum_w = mine_w, sum_r = mine_r, sum_i = mine_i;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t a = __shfl_up_sync(0xffffffffu, sum_w, o), b = __shfl_up_sync(0xffffffffu, sum_r, o);
-        if (lane >= o) { sum_w += a; sum_r += b; }
-        sum_i += __shfl_xor_sync(0xffffffffu, sum_i, o);
-      }
+      // Totals of the warps' stretches, then this CTA's stretch of the work.
+      constexpr int kWarps = kRwThreads / 32;
+      const int64_t warp_w = lane < kWarps ? S.warp_w[lane] : 0;
+      int64_t sum_w = warp_w, sum_r = lane < kWarps ? S.warp_r[lane] : 0;
+      const int64_t warp_r = sum_r, items = warp_sum(static_cast<int64_t>(lane < kWarps ? S.warp_i[lane] : 0));
+      warp_scan(sum_w, sum_r, lane);
       const int64_t weight = __shfl_sync(0xffffffffu, sum_w, 31), rows = __shfl_sync(0xffffffffu, sum_r, 31);
       bool ok = true;
       uint32_t T = 0, K = 0;  // key tiles and items so far
       const bool bad = S.bad != 0 || rows > p.rows;
       if (bad && blockIdx.x == 0 && lane == 0) atomicOr(&p.hdr->status, FD_FLAG_LEN_CLAMPED);
-      const int nact = bad || weight == 0 ? 0 : rows_active(weight, sum_i * p.hkv, static_cast<int>(gridDim.x));
+      const int nact = bad || weight == 0 ? 0 : rows_active(weight, items * p.hkv, static_cast<int>(gridDim.x));
       if (static_cast<int>(blockIdx.x) < nact) {
         const int cta = blockIdx.x;
-        const int64_t x0 = rows_bound(weight, nact, cta), x1 = rows_bound(weight, nact, cta + 1);
-        // the request that x0 falls into: its lane, its thread's stretch, then one by one
-        const unsigned at = __ballot_sync(0xffffffffu, sum_w > x0);
-        const int src = __ffs(at) - 1;  // sum_w of the last lane is weight > x0
-        int64_t base = __shfl_sync(0xffffffffu, sum_w - mine_w, src), row = __shfl_sync(0xffffffffu, sum_r - mine_r, src);
-        int t = src * (kRwThreads / 32);
-        while (base + S.part_w[t] <= x0) {
-          base += S.part_w[t];
-          row += S.part_r[t];
-          ++t;
-        }
-        int b = t * per, n, keys, prefix;
-        request(b, &n, &keys, &prefix);
+        const RowsLine line = rows_line(weight, nact);
+        const int64_t x0 = rows_bound(line, cta), x1 = rows_bound(line, cta + 1);
+        // the request that x0 falls into: its warp, its thread's stretch, then one by one
+        int src = __ffs(__ballot_sync(0xffffffffu, sum_w > x0)) - 1;  // the last lane's sum is weight > x0
+        int t = src * 32;
+        const int64_t w0 = __shfl_sync(0xffffffffu, sum_w - warp_w, src), r0 = __shfl_sync(0xffffffffu, sum_r - warp_r, src);
+        const int64_t own_w = S.part_w[t + lane], own_r = S.part_r[t + lane];
+        sum_w = own_w;
+        sum_r = own_r;
+        warp_scan(sum_w, sum_r, lane);
+        src = __ffs(__ballot_sync(0xffffffffu, w0 + sum_w > x0)) - 1;
+        t += src;
+        int64_t base = w0 + __shfl_sync(0xffffffffu, sum_w - own_w, src), row = r0 + __shfl_sync(0xffffffffu, sum_r - own_r, src);
+        int b = t * per, n = S.req[t][0], keys = S.req[t][1], prefix = S.req[t][2];
         int64_t all = p.hkv * rows_weight(kCausal, tpt, keys, rows_pairs(n, tpt));
         while (base + all <= x0) {
           base += all;
@@ -527,7 +580,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         }
         int pairs = rows_pairs(n, tpt);
         int64_t per_head = rows_weight(kCausal, tpt, keys, pairs);
-        int h = static_cast<int>((x0 - base) / per_head);
+        int h = static_cast<int>(rows_quotient(x0 - base, per_head));
         int64_t a = base + h * per_head;
         int u = 0;
         for (int hi = pairs; hi - u > 1;) {  // the last u whose items before it end at or before x0
@@ -537,6 +590,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         // The next piece of this CTA's stretch into the item ring (slot K), or the stop mark. The
         // consumers get it long before its tiles: planning takes this warp ~2500 cycles.
         bool more = true;
+        int64_t cut_a = 0, cut_w = 0;  // the published item, its key tiles if it is cut
+        int cut_tiles = 0;
         auto publish = [&](uint32_t K_) -> bool {
           const int slot = K_ & (kRwItems - 1);
           if (!row_wait(&S.iempty[slot], ((K_ / kRwItems) & 1u) ^ 1u, &S.abort_flag)) return false;
@@ -551,8 +606,9 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             const int c0 = rows_cut(x0, a0, w, tiles), c1 = rows_cut(x1, a0, w, tiles);
             if (c0 < c1) {
               found = true;
-              int cut0 = 0, cuts = 0;
-              if (c0 > 0 || c1 < tiles) rows_cuts(weight, nact, a0, w, tiles, cta, &cut0, &cuts);
+              cut_a = a0;
+              cut_w = w;
+              cut_tiles = c0 > 0 || c1 < tiles ? tiles : 0;
               const int t0 = u * 2 * tpt, nt = min(2 * tpt, n - t0);
               const bool alt = nt <= tpt;
               if (lane == 0) {
@@ -567,9 +623,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 it.k1 = k1;
                 it.prefix = prefix;
                 it.alt = alt;
-                it.cut0 = cut0;
-                it.cuts = cuts;
-                it.piece = cuts > 0 ? cta + 1 - cut0 : 0;
+                it.whole = cut_tiles == 0;
               }
               if (lane < 2) {
                 const int first = alt ? 0 : lane * tpt, tokens = alt ? nt : min(tpt, nt - first);
@@ -588,7 +642,13 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 row += n;
                 do {  // the next request with rows
                   if (++b >= p.batch) break;
-                  request(b, &n, &keys, &prefix);
+                  if (per == 1) {
+                    n = S.req[b][0];
+                    keys = S.req[b][1];
+                    prefix = S.req[b][2];
+                  } else {
+                    request(b, &n, &keys, &prefix);
+                  }
                 } while (n == 0);
                 more = b < p.batch;
                 if (more) {
@@ -604,6 +664,22 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.ifull[slot]);
           return true;
+        };
+        // How the piece's item is cut: only its output asks, so the first loads come before
+        auto publish_cuts = [&](uint32_t K_) {
+          const int slot = K_ & (kRwItems - 1);
+          if (cut_tiles > 0) {
+            int cut0, cuts;
+            rows_cuts(line, cut_a, cut_w, cut_tiles, cta, &cut0, &cuts);
+            if (lane == 0) {
+              RowItem& it = S.item[slot];
+              it.cut0 = cut0;
+              it.cuts = cuts;
+              it.piece = cta + 1 - cut0;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.cfull[slot]);
         };
         ok = publish(0);
         while (ok) {
@@ -627,6 +703,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 if (lane < kHalves) tma_load_3d(S.q[L][lane], &tmap_q, &S.qfull[L], 64 * lane, ih * p.g, q_row + L * q_step);
               }
               if (!ok) break;
+              publish_cuts(K);
             }
             if (j + 1 < c1) page = box.page(p, j + 1);
             // the ring holds two tiles: plan while they are worked on
@@ -1019,7 +1096,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         for (int a = 0; a < 4; ++a) unpair_f32(sum2[a], s[2 * a], s[2 * a + 1]);
         l = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
       }
-      if (!row_wait(&S.ofin[L], K & 1u, &S.abort_flag)) break;
+      if (!row_wait(&S.ofin[L], K & 1u, &S.abort_flag) || !row_wait(&S.cfull[slot], (K / kRwItems) & 1u, &S.abort_flag)) break;
       if (alt) {
         // the other lane's part of the row: post, meet, read, and meet again before anyone posts again
         S.xend[warp][lane] = make_float2(m, l);
