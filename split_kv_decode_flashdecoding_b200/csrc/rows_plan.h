@@ -1,8 +1,8 @@
 // How the attention of packed query rows (rows_tc.cu) is divided over the CTAs.
 //
-// Request b with n rows is cut into items of 2 T tokens, T = 128 / G: an item is up to two 128-row
+// Request b with n rows is cut into items of `span` tokens, T or 2 T with T = 128 / G: one or two 128-row
 // tiles (T tokens of all G query heads of one KV head) that walk the same key tiles. The items of
-// all (request, KV head, token pair) stand in one line, each as long as its work, counted in 1/128
+// all (request, KV head, span of tokens) stand in one line, each as long as its work, counted in 1/128
 // of a key tile plus a fixed part; CTA i of n takes the stretch [W i / n, W (i + 1) / n). An item
 // that a stretch ends in is cut at the key tile in proportion, so that every CTA has the same work
 // whatever the lengths are; its pieces are merged by the last of their CTAs to finish. A cut that
@@ -22,19 +22,29 @@ constexpr int32_t kMinPiece = 4;     // key tiles of the smallest piece of a cut
 constexpr int32_t kMaxRowCtas = 192; // CTAs of one call (merge counters in the workspace header)
 
 FD_HD int32_t rows_tile_tokens(int32_t g) { return kQTile / g; }
-FD_HD int32_t rows_pairs(int32_t n, int32_t tpt) { return cdiv32(n, 2 * tpt); }
+FD_HD int32_t rows_items(int32_t n, int32_t span) { return cdiv32(n, span); }
 
-// Work of the first u items of one (request, KV head). A prompt's item u sees 2 T (u + 1) keys, taken
+// Two row tiles an item (K and V come once for both), or one? One where two would leave CTAs without an
+// item, and where the requests' mean length fits one tile. Seen from the host, which has the sums of the
+// lengths at most. Drafted trees of 1 to 64 over 8 requests of up to 8000 keys, 8 KV heads, G 4 (64 two-tile
+// items): 61.7 us with one tile, 64.5 with two, whose pieces are twice the bytes to merge; 32 trees of 16
+// drafts, G 8, 5 to 32 K keys: 466 and 473 us.
+FD_HD bool rows_two_tiles(int32_t rows, int32_t batch, int32_t hkv, int32_t g, int32_t nctas) {
+  const int64_t t = rows_tile_tokens(g);
+  return rows > t * batch && (rows / (2 * t) + batch) * hkv >= nctas;
+}
+
+// Work of the first u items of one (request, KV head). A prompt's item u sees (u + 1) span keys, taken
 // as half a tile more on average when rounded up to tiles; every item of a tree sees all its keys.
-FD_HD int64_t rows_weight(bool causal, int32_t tpt, int32_t keys, int64_t u) {
-  return causal ? u * (kItemFixed + 64) + tpt * u * (u + 1)
+FD_HD int64_t rows_weight(bool causal, int32_t span, int32_t keys, int64_t u) {
+  return causal ? u * (kItemFixed + 64) + ((span * u * (u + 1)) >> 1)
                 : u * (kItemFixed + static_cast<int64_t>(cdiv32(keys, 128)) * 128);
 }
 
 // Keys that item u of a request sees.
-FD_HD int32_t rows_item_keys(bool causal, int32_t tpt, int32_t n, int32_t keys, int32_t u) {
+FD_HD int32_t rows_item_keys(bool causal, int32_t span, int32_t n, int32_t keys, int32_t u) {
   if (!causal) return keys;
-  const int64_t end = static_cast<int64_t>(u + 1) * 2 * tpt;
+  const int64_t end = static_cast<int64_t>(u + 1) * span;
   return end < n ? static_cast<int32_t>(end) : n;
 }
 

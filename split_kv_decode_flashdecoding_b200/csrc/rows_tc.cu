@@ -13,7 +13,8 @@
 // softmax runs, the tensor cores work for the other, so S, P and O need no second buffer and fill
 // tensor memory exactly (2 x 128 columns of S / P, 2 x D of O). An item of at most T tokens has one
 // row tile; its two lanes then take alternate key tiles and the epilogue adds their results, so a
-// small tree's softmax still runs on eight warps.
+// small tree's softmax still runs on eight warps. Where few items or short requests are known to be all
+// (rows_two_tiles), the call has one-tile items only.
 //
 // Rounding choice: P is rounded to bf16 (nearest) for the product with V, as V itself is bf16; l sums
 // the unrounded fp32 weights. The output then carries a relative error of 2^-8 of sum p |v| / l at
@@ -65,17 +66,20 @@ struct RowItem {
   int32_t cut0, cuts, piece;  // rows_cuts of the item, this piece's index
 };
 
-template <int kD>
+// kPairs: items of two row tiles. Of one tile, its Q serves both lanes, and V has a stage more for it: a V
+// stage is held through the tile's softmax.
+template <int kD, bool kPairs>
 struct __align__(1024) RwSmem {
   static constexpr int kHalves = kD / 64;
-  static constexpr int kKStages = kD == 128 ? 2 : 4;  // of K and of V
-  static constexpr int kVStages = kKStages;
-  __nv_bfloat16 q[2][kHalves][128 * 64];
+  static constexpr int kKStages = kD == 128 ? 2 : 4;
+  static constexpr int kVStages = kPairs ? kKStages : kD == 128 ? 3 : 6;
+  static constexpr int kQ = kPairs ? 2 : 1;
+  __nv_bfloat16 q[kQ][kHalves][128 * 64];
   __nv_bfloat16 k[kKStages][kHalves][128 * 64];
   __nv_bfloat16 v[kVStages][kHalves][128 * 64];
   RowItem item[kRwItems];
   int32_t req[kRwThreads][3];  // a thread's first request: rows, keys, prefix
-  float2 xend[8][32];  // softmax warps: a row's (m, l) at the end of an alt item, for the other lane's warp
+  float2 xend[2][8][32];  // softmax warps: a row's (m, l) at the end of an alt item, for the other lane's warp
   union {
     struct {  // plan: work and rows of a thread's requests; work, rows and items of a warp's
       int64_t part_w[kRwThreads], warp_w[kRwThreads / 32];
@@ -93,8 +97,10 @@ struct __align__(1024) RwSmem {
   int abort_flag;
   int bad;
 };
-static_assert(sizeof(RwSmem<128>) + 1024 <= 227 * 1024, "row attention shared memory");
-static_assert(sizeof(RwSmem<64>) + 1024 <= 227 * 1024, "row attention shared memory");
+static_assert(sizeof(RwSmem<128, true>) + 1024 <= 227 * 1024, "row attention shared memory");
+static_assert(sizeof(RwSmem<128, false>) + 1024 <= 227 * 1024, "row attention shared memory");
+static_assert(sizeof(RwSmem<64, true>) + 1024 <= 227 * 1024, "row attention shared memory");
+static_assert(sizeof(RwSmem<64, false>) + 1024 <= 227 * 1024, "row attention shared memory");
 
 // ---- arithmetic on pairs of fp32 ------------------------------------------------------------------
 
@@ -224,6 +230,22 @@ __device__ __forceinline__ void visible_words(const RowsParams& p, const RowItem
   }
 }
 
+// 1 / l; 0 for an empty row; NaN stays.
+__device__ __forceinline__ float row_over(float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); }
+
+// Where a thread stores: 16 bytes of rows lane / 4 + 8 i of its warp's (null: behind the last token). Found
+// before O is complete.
+__device__ __forceinline__ void row_places(const RowsParams& p, const RowItem& it, int quad, int lane, int t, int tpt, char* (&dst)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rr = quad * 32 + (lane >> 2) + 8 * i, pos = (rr * p.g_recip16) >> 16;
+    dst[i] = pos < it.tokens[t] ? static_cast<char*>(p.out) + 2 * ((static_cast<int64_t>(it.row0) + pos + t * tpt) * p.o_sr +
+                                                                   static_cast<int64_t>(it.h * p.g + rr - pos * p.g) * p.o_sh) +
+                                      16 * (lane & 3)
+                                : nullptr;
+  }
+}
+
 // The end of an item for one softmax warp: columns [c0, c1) of its 32 rows of row tile t, the
 // accumulator at o_col (an alt item: both lanes', times f0 and f1) over l, to memory; or, for a piece of
 // a cut item, unscaled to the workspace, where the warp that counts the last piece adds them all in
@@ -233,19 +255,10 @@ __device__ __forceinline__ void visible_words(const RowsParams& p, const RowItem
 // code runs once an item, from a cold instruction cache.
 template <int kD, bool kAlt, typename Smem>
 __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const RowItem& it, int warp, int lane, int t,
-                                           int c0, int c1, uint32_t o_col, int tpt, float m, float l, float f0, float f1) {
+                                           int c0, int c1, uint32_t o_col, int tpt, char* const (&dst)[4], float m, float l,
+                                           float scale, float f0, float f1) {
   const int quad = warp & 3;
   uint4* stage = S.stage[warp];
-  // this thread's stores: 16 bytes of rows lane / 4 + 8 i
-  char* dst[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int rr = quad * 32 + (lane >> 2) + 8 * i, pos = (rr * p.g_recip16) >> 16;
-    dst[i] = pos < it.tokens[t] ? static_cast<char*>(p.out) + 2 * ((static_cast<int64_t>(it.row0) + pos + t * tpt) * p.o_sr +
-                                                                   static_cast<int64_t>(it.h * p.g + rr - pos * p.g) * p.o_sh) +
-                                      16 * (lane & 3)
-                                : nullptr;
-  }
   auto emit = [&](int c, const uint64_t (&o)[16]) {
     uint32_t w[16];
 #pragma unroll
@@ -271,7 +284,6 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
       p.lse[(static_cast<int64_t>(it.row0) + pos + t * tpt) * p.hq + it.h * p.g + r - pos * p.g] =
           l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   };
-  auto over = [](float l) { return l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l); };  // 0 for an empty row; NaN stays
   const bool live = (((quad * 32 + lane) * p.g_recip16) >> 16) < it.tokens[t];  // this thread's row
   // pieces: O as [slot][row tile][D / 4][128 rows] float4, (m, l) as [slot][warp][32 rows] float2
   ulonglong2* part_o = reinterpret_cast<ulonglong2*>(p.part_o) + quad * 32 + lane;
@@ -281,23 +293,21 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
   const bool whole = it.whole != 0;
   // A lane without tiles has left its accumulator as it was: that one is not looked at.
   const bool none0 = it.used[kAlt ? 0 : t] == 0, none1 = it.used[1] == 0;
-  const float scale = whole ? over(l) : 1.f;
   const uint64_t s02 = pair_f32(scale * f0, scale * f0), s12 = pair_f32(scale * f1, scale * f1);
 #pragma unroll 1
   for (int c = c0; c < c1; c += 32) {
     uint64_t o[16];
-    uint32_t raw[32];
+    uint32_t raw[32], raw1[32];
     tmem_ld32(o_col + c, raw);
+    if (kAlt) tmem_ld32(o_col + kD + c, raw1);
     tmem_wait_ld();
 #pragma unroll
     for (int e = 0; e < 16; ++e)
       o[e] = none0 ? 0ull : fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s02, 0ull);
     if (kAlt && !none1) {
-      tmem_ld32(o_col + kD + c, raw);
-      tmem_wait_ld();
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        o[e] = fma_f32x2(pair_f32(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])), s12, o[e]);
+        o[e] = fma_f32x2(pair_f32(__uint_as_float(raw1[2 * e]), __uint_as_float(raw1[2 * e + 1])), s12, o[e]);
     }
     if (c + 32 >= c1) {  // the accumulator is read: the next item's first product may start
       tc_fence_before();
@@ -347,7 +357,7 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
       if (!(ml[i].y == 0.f)) lt = fmaf(ml[i].y, fast_exp2(ml[i].x - mn), lt);
     mt = mn;
   }
-  const float total = over(lt);
+  const float total = row_over(lt);
 #pragma unroll 1
   for (int c = c0; c < c1; c += 32) {
     uint64_t o[16];
@@ -424,18 +434,19 @@ struct KeyBoxes {
   }
 };
 
-template <int kD, int kSrc>
+template <int kD, int kSrc, bool kPairs>
 __global__ void __launch_bounds__(kRwThreads, 1)
     rows_tc_kernel(const RowsParams p, const __grid_constant__ CUtensorMap tmap_q,
                    const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v) {
-  using Smem = RwSmem<kD>;
+  using Smem = RwSmem<kD, kPairs>;
   constexpr bool kCausal = kSrc == kSrcPacked;
   constexpr int kHalves = Smem::kHalves, kKStages = Smem::kKStages, kVStages = Smem::kVStages;
+  constexpr int kQ = Smem::kQ;  // row tiles of an item
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, and known to be
-  const int tpt = rows_tile_tokens(p.g);
+  const int tpt = rows_tile_tokens(p.g), span = kQ * tpt;
 
   if (tid == 0) {
     for (int s = 0; s < Smem::kKStages; ++s) {
@@ -506,10 +517,10 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       if (b >= p.batch) break;
       int n, keys, prefix;
       flag |= request(b, &n, &keys, &prefix);
-      const int pairs = rows_pairs(n, tpt);
-      w += p.hkv * rows_weight(kCausal, tpt, keys, pairs);
+      const int parts = rows_items(n, span);
+      w += p.hkv * rows_weight(kCausal, span, keys, parts);
       rows += n;
-      items += pairs;
+      items += parts;
       if (i == 0) {
         S.req[tid][0] = n;
         S.req[tid][1] = keys;
@@ -571,21 +582,21 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         t += src;
         int64_t base = w0 + __shfl_sync(0xffffffffu, sum_w - own_w, src), row = r0 + __shfl_sync(0xffffffffu, sum_r - own_r, src);
         int b = t * per, n = S.req[t][0], keys = S.req[t][1], prefix = S.req[t][2];
-        int64_t all = p.hkv * rows_weight(kCausal, tpt, keys, rows_pairs(n, tpt));
+        int64_t all = p.hkv * rows_weight(kCausal, span, keys, rows_items(n, span));
         while (base + all <= x0) {
           base += all;
           row += n;
           request(++b, &n, &keys, &prefix);
-          all = p.hkv * rows_weight(kCausal, tpt, keys, rows_pairs(n, tpt));
+          all = p.hkv * rows_weight(kCausal, span, keys, rows_items(n, span));
         }
-        int pairs = rows_pairs(n, tpt);
-        int64_t per_head = rows_weight(kCausal, tpt, keys, pairs);
+        int parts = rows_items(n, span);
+        int64_t per_head = rows_weight(kCausal, span, keys, parts);
         int h = static_cast<int>(rows_quotient(x0 - base, per_head));
         int64_t a = base + h * per_head;
         int u = 0;
-        for (int hi = pairs; hi - u > 1;) {  // the last u whose items before it end at or before x0
+        for (int hi = parts; hi - u > 1;) {  // the last u whose items before it end at or before x0
           const int mid = (u + hi) >> 1;
-          if (a + rows_weight(kCausal, tpt, keys, mid) <= x0) u = mid; else hi = mid;
+          if (a + rows_weight(kCausal, span, keys, mid) <= x0) u = mid; else hi = mid;
         }
         // The next piece of this CTA's stretch into the item ring (slot K), or the stop mark. The
         // consumers get it long before its tiles: planning takes this warp ~2500 cycles.
@@ -598,10 +609,10 @@ __global__ void __launch_bounds__(kRwThreads, 1)
           RowItem& it = S.item[slot];
           bool found = false;
           while (more && !found) {
-            const int64_t a0 = a + rows_weight(kCausal, tpt, keys, u);
+            const int64_t a0 = a + rows_weight(kCausal, span, keys, u);
             if (a0 >= x1) break;
-            const int64_t w = a + rows_weight(kCausal, tpt, keys, u + 1) - a0;
-            const int k1 = rows_item_keys(kCausal, tpt, n, keys, u);
+            const int64_t w = a + rows_weight(kCausal, span, keys, u + 1) - a0;
+            const int k1 = rows_item_keys(kCausal, span, n, keys, u);
             const int tiles = (k1 + 127) >> 7;
             const int c0 = rows_cut(x0, a0, w, tiles), c1 = rows_cut(x1, a0, w, tiles);
             if (c0 < c1) {
@@ -609,8 +620,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
               cut_a = a0;
               cut_w = w;
               cut_tiles = c0 > 0 || c1 < tiles ? tiles : 0;
-              const int t0 = u * 2 * tpt, nt = min(2 * tpt, n - t0);
-              const bool alt = nt <= tpt;
+              const int t0 = u * span, nt = min(span, n - t0);
+              const bool alt = !kPairs || nt <= tpt;
               if (lane == 0) {
                 it.stop = 0;
                 it.b = b;
@@ -633,7 +644,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 it.used[lane] = alt ? (c1 - c0 + 1 - lane) >> 1 : max(0, min(c1 - c0, (kend + 127) >> 7));
               }
             }
-            if (++u == pairs) {
+            if (++u == parts) {
               u = 0;
               a += per_head;
               if (++h == p.hkv) {
@@ -652,8 +663,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
                 } while (n == 0);
                 more = b < p.batch;
                 if (more) {
-                  pairs = rows_pairs(n, tpt);
-                  per_head = rows_weight(kCausal, tpt, keys, pairs);
+                  parts = rows_items(n, span);
+                  per_head = rows_weight(kCausal, span, keys, parts);
                   all = p.hkv * per_head;
                   a = base;
                 }
@@ -696,8 +707,9 @@ __global__ void __launch_bounds__(kRwThreads, 1)
             box.load(p, &tmap_k, &S.kfull[st], S.k[st][0], j, page);
             if (j == c0) {
 #pragma unroll 1
-              for (int L = 0; L < 2; ++L) {
-                if (!row_wait(&S.qempty[L], (K & 1u) ^ 1u, &S.abort_flag)) { ok = false; break; }
+              for (int L = 0; L < kQ; ++L) {
+                if (!row_wait(&S.qempty[L], (K & 1u) ^ 1u, &S.abort_flag) ||
+                    (!kPairs && !row_wait(&S.qempty[1], (K & 1u) ^ 1u, &S.abort_flag))) { ok = false; break; }
                 if (lane == 0) mbar_arrive_expect_tx(&S.qfull[L], kHalves * 128u * static_cast<uint32_t>(p.g * p.q_box_rows));
                 __syncwarp();
                 if (lane < kHalves) tma_load_3d(S.q[L][lane], &tmap_q, &S.qfull[L], 64 * lane, ih * p.g, q_row + L * q_step);
@@ -720,7 +732,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       __syncwarp();
       if (S.abort_flag && lane == 0) {  // copies still in flight land before the CTA leaves
         for (uint32_t back = 1; back <= kKStages && back <= T; ++back) (void)row_poll(&S.kfull[(T - back) % kKStages], ((T - back) / kKStages) & 1u);
-        for (int L = 0; L < 2; ++L) {
+        for (int L = 0; L < kQ; ++L) {
           if (K > 0) (void)row_poll(&S.qfull[L], (K - 1) & 1u);
           (void)row_poll(&S.qfull[L], K & 1u);
         }
@@ -784,7 +796,7 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         const uint32_t st = t % kKStages;
         if (!row_wait_warp(&S.kfull[st], (t / kKStages) & 1u, &S.abort_flag)) return false;
         tc_fence_after();
-        const uint64_t qd = q_desc + static_cast<uint64_t>(L * kTileDesc), kd = k_desc + static_cast<uint64_t>(st * kTileDesc);
+        const uint64_t qd = q_desc + static_cast<uint64_t>(kPairs ? L * kTileDesc : 0), kd = k_desc + static_cast<uint64_t>(st * kTileDesc);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kD / 16; ++kk) {
@@ -839,8 +851,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       // a tile of the lane, after the product that is still to issue
       auto begin = [&](auto lane_no, Turn& st, uint32_t K, uint32_t t, int tile, bool alone) -> bool {
         constexpr int L = decltype(lane_no)::value;
-        if (st.i == 0 && !row_wait_warp(&S.qfull[L], K & 1u, &S.abort_flag)) return false;
-        if (st.pend != 0 && !product(lane_no, st)) return false;
+        if (st.pend != 0 && !product(lane_no, st)) return false;  // first: its output waits for it
+        if (st.i == 0 && !row_wait_warp(&S.qfull[kPairs ? L : 0], K & 1u, &S.abort_flag)) return false;
         if (!scores(lane_no, t)) return false;
         started(lane_no, st, K, t, tile, alone);
         return true;
@@ -848,9 +860,9 @@ __global__ void __launch_bounds__(kRwThreads, 1)
       // an item that gives the lane nothing to do: its Q goes back unread, its (empty) O is there
       auto skip = [&](auto lane_no, Turn& st, uint32_t K) -> bool {
         constexpr int L = decltype(lane_no)::value;
-        if (!row_wait_warp(&S.qfull[L], K & 1u, &S.abort_flag)) return false;
-        if (lane == 0) mbar_arrive(&S.qempty[L]);
         if (st.pend != 0 && !product(lane_no, st)) return false;
+        if (!row_wait_warp(&S.qfull[kPairs ? L : 0], K & 1u, &S.abort_flag)) return false;
+        if (lane == 0) mbar_arrive(&S.qempty[L]);
         if (!row_wait_warp(&S.oempty[L], (K & 1u) ^ 1u, &S.abort_flag)) return false;
         if (lane == 0) mbar_arrive(&S.ofin[L]);
         return true;
@@ -863,7 +875,8 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         const RowItem& it = S.item[slot];
         const auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
         if (uniform(it.stop)) break;
-        const int ntile = uniform(it.ntile), alt = uniform(it.alt);
+        const int ntile = uniform(it.ntile);
+        const bool alt = !kPairs || uniform(it.alt);
         st0.i = st1.i = 0;
         st0.used = uniform(it.used[0]);
         st1.used = uniform(it.used[1]);
@@ -871,12 +884,12 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         st1.kend = uniform(it.kend[1]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.iempty[slot]);
-        if (alt) {
+        if (!kPairs || alt) {
 #pragma unroll 1
           for (int j = 0; ok && j < ntile; ++j)
             ok = (j & 1) == 0 ? begin(lane0, st0, K, T + j, j, true) : begin(lane1, st1, K, T + j, j, true);
           if (ok && st1.used == 0) ok = skip(lane1, st1, K);
-        } else {
+        } else if constexpr (kPairs) {
           // lane 1 uses every tile, lane 0 all but the last or all
           const int n0 = st0.used;
           if (n0 > 0) ok = begin(lane0, st0, K, T, 0, false);
@@ -960,14 +973,15 @@ __global__ void __launch_bounds__(kRwThreads, 1)
     const uint32_t o_base = tmem + lane_base + kRwColO, s_col = tmem + lane_base + 128 * L, o_col = o_base + kD * L;
     const int pos_in = (r * p.g_recip16) >> 16;  // r / G
     const uint64_t scale2 = pair_f32(p.scale_log2, p.scale_log2);
-    uint32_t T = 0, J = 0;
+    uint32_t T = 0, J = 0, X = 0;  // key tiles, the lane's tiles, exchanges
     bool ok = true;
     for (uint32_t K = 0; ok; ++K) {
       const int slot = K & (kRwItems - 1);
       if (!row_wait(&S.ifull[slot], (K / kRwItems) & 1u, &S.abort_flag)) break;
       const RowItem& it = S.item[slot];  // stays in shared memory: the scores need the registers
       if (it.stop) break;
-      const int used = it.used[L], alt = it.alt;
+      const int used = it.used[L];
+      const bool alt = !kPairs || it.alt;
       const int both = alt ? 0 : it.used[0];        // tiles that both lanes use
       const int pos = pos_in + (alt ? 0 : L * tpt);  // token of the item
       const bool row_ok = pos_in < it.tokens[L];
@@ -1096,27 +1110,33 @@ __global__ void __launch_bounds__(kRwThreads, 1)
         for (int a = 0; a < 4; ++a) unpair_f32(sum2[a], s[2 * a], s[2 * a + 1]);
         l = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
       }
-      if (!row_wait(&S.ofin[L], K & 1u, &S.abort_flag) || !row_wait(&S.cfull[slot], (K / kRwItems) & 1u, &S.abort_flag)) break;
+      // While the last product runs: the row's own part of the output, and where it goes.
       if (alt) {
-        // the other lane's part of the row: post, meet, read, and meet again before anyone posts again
-        S.xend[warp][lane] = make_float2(m, l);
+        // the other lane's part of the row: post, meet, read. The next post but one finds it read: it comes
+        // after the next meeting.
+        S.xend[X & 1u][warp][lane] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.xpair[quad]);
-        if (!row_wait(&S.xpair[quad], 0u, &S.abort_flag)) break;
-        const float2 y = S.xend[warp ^ 4][lane];
+      }
+      char* dst[4];
+      row_places(p, it, quad, lane, alt ? 0 : L, tpt, dst);
+      if (alt) {
+        if (!row_wait(&S.xpair[quad], X & 1u, &S.abort_flag)) break;
+        const float2 y = S.xend[X & 1u][warp ^ 4][lane];
+        ++X;
         const float ma = L == 0 ? m : y.x, mb = L == 0 ? y.x : m, la = L == 0 ? l : y.y, lb = L == 0 ? y.y : l;
         m = fmaxf(ma, mb);
         f0 = la == 0.f ? 0.f : fast_exp2(ma - m);
         f1 = lb == 0.f ? 0.f : fast_exp2(mb - m);
         l = la * f0 + lb * f1;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.xpair[quad]);
-        if (!row_wait(&S.xpair[quad], 1u, &S.abort_flag)) break;
-        if (!row_wait(&S.ofin[L ^ 1], K & 1u, &S.abort_flag)) break;
       }
+      const float scale = it.whole ? row_over(l) : 1.f;
+      if (!row_wait(&S.ofin[L], K & 1u, &S.abort_flag) || (alt && !row_wait(&S.ofin[L ^ 1], K & 1u, &S.abort_flag)) ||
+          !row_wait(&S.cfull[slot], (K / kRwItems) & 1u, &S.abort_flag))
+        break;
       tc_fence_after();
-      if (alt) row_output<kD, true>(p, S, it, warp, lane, 0, L * (kD / 2), (L + 1) * (kD / 2), o_base, tpt, m, l, f0, f1);
-      else row_output<kD, false>(p, S, it, warp, lane, L, 0, kD, o_col, tpt, m, l, 1.f, 0.f);
+      if (alt) row_output<kD, true>(p, S, it, warp, lane, 0, L * (kD / 2), (L + 1) * (kD / 2), o_base, tpt, dst, m, l, scale, f0, f1);
+      else if constexpr (kPairs) row_output<kD, false>(p, S, it, warp, lane, L, 0, kD, o_col, tpt, dst, m, l, scale, 1.f, 0.f);
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.iempty[slot]);
     }
@@ -1129,11 +1149,11 @@ __global__ void __launch_bounds__(kRwThreads, 1)
   if (warp == kRwIssue) tmem_dealloc(tmem, kRwTmemCols);
 }
 
-template <int kD, int kSrc>
+template <int kD, int kSrc, bool kPairs>
 cudaError_t launch_rows_t(const RowsParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                           int nctas, cudaStream_t stream) {
-  const size_t smem = sizeof(RwSmem<kD>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<kD, kSrc>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const size_t smem = sizeof(RwSmem<kD, kPairs>) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(rows_tc_kernel<kD, kSrc, kPairs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -1146,7 +1166,7 @@ cudaError_t launch_rows_t(const RowsParams& p, const CUtensorMap& tq, const CUte
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rows_tc_kernel<kD, kSrc>, p, tq, tk, tv);
+  return cudaLaunchKernelEx(&cfg, rows_tc_kernel<kD, kSrc, kPairs>, p, tq, tk, tv);
 }
 
 }  // namespace
@@ -1161,14 +1181,17 @@ cudaError_t launch_rows(RowsParams p, const CUtensorMap& tq, const CUtensorMap& 
   p.part_o = reinterpret_cast<float*>(base + sizeof(WsHeader));
   p.part_ml = p.part_o + static_cast<int64_t>(2 * nctas) * 2 * 128 * p.d;
   const int src = p.prefix_lens == nullptr ? kSrcPacked : p.block_table ? kSrcPaged : kSrcCache;
-  if (p.d == 128) {
-    if (src == kSrcPacked) return launch_rows_t<128, kSrcPacked>(p, tq, tk, tv, nctas, stream);
-    if (src == kSrcCache) return launch_rows_t<128, kSrcCache>(p, tq, tk, tv, nctas, stream);
-    return launch_rows_t<128, kSrcPaged>(p, tq, tk, tv, nctas, stream);
-  }
-  if (src == kSrcPacked) return launch_rows_t<64, kSrcPacked>(p, tq, tk, tv, nctas, stream);
-  if (src == kSrcCache) return launch_rows_t<64, kSrcCache>(p, tq, tk, tv, nctas, stream);
-  return launch_rows_t<64, kSrcPaged>(p, tq, tk, tv, nctas, stream);
+  const auto launch = [&](auto d, auto pairs) {
+    constexpr int kD = decltype(d)::value;
+    constexpr bool kPairs = decltype(pairs)::value;
+    if (src == kSrcPacked) return launch_rows_t<kD, kSrcPacked, kPairs>(p, tq, tk, tv, nctas, stream);
+    if (src == kSrcCache) return launch_rows_t<kD, kSrcCache, kPairs>(p, tq, tk, tv, nctas, stream);
+    return launch_rows_t<kD, kSrcPaged, kPairs>(p, tq, tk, tv, nctas, stream);
+  };
+  const std::integral_constant<int, 128> d128{};
+  const std::integral_constant<int, 64> d64{};
+  if (rows_two_tiles(p.rows, p.batch, p.hkv, p.g, nctas)) return p.d == 128 ? launch(d128, std::true_type{}) : launch(d64, std::true_type{});
+  return p.d == 128 ? launch(d128, std::false_type{}) : launch(d64, std::false_type{});
 }
 
 }  // namespace fd

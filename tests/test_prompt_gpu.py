@@ -171,3 +171,10 @@ def test_on_another_stream_beside_the_current_one():
         here = fd.fd_prompt_attention(q, k, v, n)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(want, got, here))
+
+
+# enough tokens and heads for items of two row tiles, next to requests of one tile, of one token and of none
+@pytest.mark.parametrize("hq,hkv,lens", [(40, 40, [1500, 0, 130, 257, 1]), (64, 8, [777, 16, 33, 0, 1025]), (96, 48, [64, 65, 129, 900])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_two_row_tiles(hq, hkv, lens, d):
+    _check(lens, hq, hkv, d, seed=13, pad=5)

@@ -220,3 +220,13 @@ def test_same_results_again_and_in_a_graph():
     # other lengths may cut the first request's keys elsewhere: the bounds hold, not every bit
     ref.check_rows(out[:16], lse[:16], ref.tree(c.q[:16], c.caches[:1], c.prefix[:1], [16], c.see[:1]))
     assert fd.fd_poll_status(stream=s) == 0
+
+
+# enough tokens and heads for items of two row tiles (more tokens than a tile a request, an item a
+# multiprocessor), next to requests of one tile and of none, with cuts inside the drafts
+@pytest.mark.parametrize("hq,hkv,new", [(64, 8, [64, 33, 1, 0, 64, 48, 64, 17, 64, 50]), (40, 40, [256, 129, 1, 128, 255]),
+                                        (96, 48, [65, 128, 200, 0, 64])])
+@pytest.mark.parametrize("d,page", [(128, 16), (64, 128), (128, 0), (64, 0)])
+def test_two_row_tiles(hq, hkv, new, d, page):
+    prefix = [(977 * i + 300) % 2000 for i in range(len(new))]
+    Case(prefix, new, hq, hkv, d, page=page, seed=12, pad=3).check()
