@@ -85,7 +85,8 @@ typedef struct {
 
 /* Device status word bits (fd_poll_status). */
 #define FD_FLAG_LEN_CLAMPED 0x1u  /* some cache/prefix/chunk length was outside [0, S_cap]     */
-#define FD_FLAG_WAIT_TIMEOUT 0x2u /* a kernel wait gave up; the call's results are invalid     */
+#define FD_FLAG_WAIT_TIMEOUT 0x2u /* a kernel wait gave up: the call's results, and those of the
+                                      stream's calls up to this poll, are invalid             */
 #define FD_FLAG_PLAN_OVERFLOW 0x4u /* the device plan exceeded the workspace bound (a bug)     */
 #define FD_FLAG_BAD_PAGE 0x8u      /* a block-table entry of a used page was outside the pool   */
 #define FD_FLAG_POOL_FULL 0x10u    /* a page operator ran out of free pages                    */
@@ -359,6 +360,7 @@ size_t fd_prompt_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_
  *  tree_mask    [T][mask_words] 32-bit words (device, contiguous), 1 <= mask_words <= 8.
  *  out, lse     as in fd_prompt_attention.
  * v must be finite at a request's keys [0, prefix + tree_len); what stands behind may be anything.
+ * T and S_cap are at most 2^31 - 1024.
  */
 fd_status fd_tree_attention(const fd_tensor* q, const fd_tensor* k_cache, const fd_tensor* v_cache,
                             const int32_t* prefix_lens, const int32_t* tree_lens,

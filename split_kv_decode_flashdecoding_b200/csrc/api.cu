@@ -1016,6 +1016,8 @@ fd_status fd_poll_status(void* stream_, uint32_t* flags) {
     FD_CUDA(cudaMemcpy(&one, ptr, sizeof(one), cudaMemcpyDeviceToHost), "read status");
     const uint32_t zero = 0;
     FD_CUDA(cudaMemcpy(ptr, &zero, sizeof(zero), cudaMemcpyHostToDevice), "clear status");
+    if (one & FD_FLAG_WAIT_TIMEOUT)  // a call that gave up may have left pieces counted
+      FD_CUDA(cudaMemset(static_cast<char*>(ptr) + offsetof(WsHeader, row_pieces), 0, sizeof(WsHeader::row_pieces)), "clear counters");
     v |= one;
   }
   // the status bits of fd_decode_attention_static calls on this device

@@ -12,6 +12,7 @@ using namespace fd_abi;
 namespace {
 
 constexpr int32_t kMaxMaskWords = 8;
+constexpr int64_t kMaxKeys = (int64_t{1} << 31) - 1024;  // the kernel counts keys up to whole tiles in 32 bits
 
 fd_status check_rows(const fd_tensor* t, const char* name, int64_t rows, int64_t heads, int64_t d) {
   fd_status s;
@@ -37,6 +38,7 @@ fd_status resolve_rows(const fd_tensor* q, const fd_tensor* out, int64_t hkv, in
   if (hq < 1 || hq % hkv != 0)
     return fail(FD_ERR_INVALID_ARGUMENT, "q heads (%lld) must be a positive multiple of KV heads (%lld)", (long long)hq, (long long)hkv);
   if (hq / hkv > 16) return fail(FD_ERR_UNSUPPORTED, "group size %lld above 16", (long long)(hq / hkv));
+  if (rows > kMaxKeys) return fail(FD_ERR_UNSUPPORTED, "more than 2^31 - 1024 rows");
   if (hq > 65535) return fail(FD_ERR_UNSUPPORTED, "more than 65535 query heads");
   if (batch < 0) return fail(FD_ERR_INVALID_ARGUMENT, "batch must be >= 0");
   if (batch > kMaxPlanBatch) return fail(FD_ERR_UNSUPPORTED, "batch %d exceeds %d", batch, kMaxPlanBatch);
@@ -127,6 +129,7 @@ fd_status tree(const fd_tensor* q, const fd_tensor* k, const fd_tensor* v, const
   } else {
     p.cap = static_cast<int32_t>(k->shape[2]);
   }
+  if (p.cap > kMaxKeys) return fail(FD_ERR_UNSUPPORTED, "a capacity of %d keys exceeds 2^31 - 1024", p.cap);
   if (p.rows == 0 || p.batch == 0) return FD_OK;
   if (!prefix_lens || !tree_lens || !tree_mask)
     return fail(FD_ERR_INVALID_ARGUMENT, "prefix_lens / tree_lens / tree_mask is NULL");

@@ -178,3 +178,51 @@ def test_on_another_stream_beside_the_current_one():
 @pytest.mark.parametrize("d", [64, 128])
 def test_two_row_tiles(hq, hkv, lens, d):
     _check(lens, hq, hkv, d, seed=13, pad=5)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(40, 40, 128), (40, 40, 64), (64, 8, 128)])
+def test_non_finite_values_in_two_row_tiles(hq, hkv, d):
+    fd = _fd()
+    lens = [500, 130, 300]
+    q, k, v = _inputs(lens, hq, hkv, d, 14)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    good = fd.fd_prompt_attention(q, k, v, n)
+    k[500:630], v[500:630] = NAN, float("inf")  # another request's
+    bad = fd.fd_prompt_attention(q, k, v, n)
+    for a, b in zip(good, bad):
+        assert torch.equal(a[:500], b[:500]) and torch.equal(a[630:], b[630:])
+    for value in (NAN, float("inf"), float("-inf")):
+        k[630 + 140] = value
+        bad = fd.fd_prompt_attention(q, k, v, n)
+        for a, b in zip(good, bad):
+            assert torch.equal(a[:500], b[:500]) and torch.equal(a[630:770], b[630:770])
+            if value != value:
+                assert bool(b[770:].isnan().all())
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(64, 8, 128), (40, 40, 64)])
+def test_two_row_tiles_in_a_graph(hq, hkv, d):
+    fd = _fd()
+    lens = [700, 0, 45, 1333]
+    q, k, v = _inputs(lens, hq, hkv, d, 15)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fd.fd_reserve_workspace(fd.fd_prompt_workspace_bytes(4, sum(lens), hq, hkv, d), stream=s)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            fd.fd_prompt_attention(q, k, v, n, out=out, lse=lse)
+    # the kernel of the padded batch stays that of its rows, whatever the lengths of a replay
+    for new in ([700, 0, 45, 1333], [1, 2, 3, 4], [2078, 0, 0, 0], [0, 1, 0, 0]):
+        n.copy_(torch.tensor(new, dtype=torch.int32))
+        out.fill_(9.0), lse.fill_(9.0)
+        torch.cuda.synchronize()
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        t = sum(new)
+        assert bool((out[t:] == 9.0).all()) and bool((lse[t:] == 9.0).all())
+        ref.check_rows(out[:t], lse[:t], ref.prompt(q[:t], k[:t], v[:t], new))
+    assert fd.fd_poll_status(stream=s) == 0

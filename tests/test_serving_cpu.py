@@ -233,3 +233,15 @@ def test_workspace_sizes():
     assert fd.fd_tree_workspace_bytes(3, 100, 8, 2, 500, 128) >= 256
     assert fd.fd_prompt_workspace_bytes(-1, 100, 8, 2, 128) == 0
     assert fd.fd_tree_workspace_bytes(3, -1, 8, 2, 500, 128) == 0
+
+
+def test_capacities_near_2_to_the_31_are_refused():
+    big = 2**31 - 1023
+    assert _prompt(q=_fake((big, 8, 128), strides=[0, 128, 1]), out=_fake((big, 8, 128), strides=[0, 128, 1])) == UNS
+
+    def tree(pages, page_size):
+        kv = _fake((4, 2, page_size, 64))
+        q = _fake((3, 4, 64))
+        return fd.lib.fd_tree_attention_paged(_ref(q), _ref(kv), _ref(kv), _i(), pages, 1, _i(), _i(), _i(), 1, _ref(q), _f(), None)
+
+    assert tree((2**31 - 1024) // 8 + 1, 8) == UNS and tree(2**31 // 128 - 1, 128) == UNS
