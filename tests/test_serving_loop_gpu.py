@@ -75,3 +75,32 @@ def test_serving_run(hq, hkv, d, size):
     fd.fd_pages_free(refs, table, lens, _i32(list(range(seqs))))
     assert not refs.any() and not lens.any() and bool((table < 0).all())
     assert fd.fd_poll_status() == 0
+
+
+def test_places_behind_2_to_the_31_elements():
+    import split_kv_decode_flashdecoding_b200 as fd
+    pages, hkv, size, d, hq = 16400, 8, 128, 128, 16
+    taken = (1 << 31) // (hkv * size * d)  # the pages from here on lie behind 2^31 elements
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    k_pages = torch.zeros((pages, hkv, size, d), dtype=torch.bfloat16, device="cuda")
+    v_pages, refs, table = torch.zeros_like(k_pages), _i32([1] * taken + [0] * (pages - taken)), _i32([[-1] * 4] * 2)
+    prefix, new = 300, 5
+    q, k, v = (torch.randn((prefix + new, h, d), generator=gen, device="cuda").to(torch.bfloat16) for h in (hq, hkv, hkv))
+    fd.fd_pages_reserve(refs, table, _i32([prefix + new, 0]), size)
+    assert table.tolist() == [[taken, taken + 1, taken + 2, -1], [-1] * 4]
+    fd.fd_pages_append(k, v, k_pages, v_pages, table, _i32([0, 0]), _i32([prefix + new, 0]))
+    lens = _i32([prefix + new, 0])
+    fd.fd_pages_fork(k_pages, v_pages, refs, table, lens, _i32([0]), _i32([1]))
+    assert table.tolist() == [[taken, taken + 1, taken + 2, -1], [taken, taken + 1, taken + 3, -1]]
+    see = [ref.random_tree(torch.Generator().manual_seed(32), new)] * 2
+    drafts = torch.cat([q[prefix:]] * 2)
+    out, lse = fd.fd_tree_attention_paged(drafts, k_pages, v_pages, table, _i32([prefix] * 2), _i32([new] * 2),
+                                          ref.mask_words(see, 1).cuda())
+    ref.check_rows(out, lse, ref.tree(drafts, [(k, v)] * 2, [prefix] * 2, [new] * 2, see), "tree")
+    fd.fd_pages_compact(k_pages, v_pages, refs, table, lens, _i32([prefix, 0]), _i32([[1, 4], [0, 0]]), _i32([2, -1]))
+    assert lens.tolist() == [prefix + 2, prefix + new]
+    for pool, x in ((k_pages, k), (v_pages, v)):
+        for page, rows in ((taken + 2, [*range(256, 300), 301, 304]), (taken + 3, [*range(256, 305)])):
+            assert torch.equal(pool[page, :, :len(rows)], x[rows].transpose(0, 1))
+        assert not bool(pool[:taken].any()) and not bool(pool[taken + 4:].any())
+    assert fd.fd_poll_status() == 0
