@@ -1,7 +1,8 @@
 """Python binding of the split-KV FlashDecoding C ABI (include/fd.h).
 
-Argument marshalling only: every step of the attention path runs in the CUDA kernels of
-libfd.so. PyTorch supplies device memory and streams. Importing this package fails loudly when
+Argument marshalling only (through ctypes, and for the serving calls, which host time would bound on
+short batches, through a compiled module): every step of the attention path runs in the CUDA kernels
+of libfd.so. PyTorch supplies device memory and streams. Importing this package fails loudly when
 libfd.so has not been built (``python split_kv_decode_flashdecoding_b200/build.py``); there is no
 CPU fallback.
 
@@ -22,8 +23,8 @@ Functions keep the C names:
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
-import struct
 from typing import List, Optional, Sequence, Tuple
 
 import torch
@@ -139,6 +140,14 @@ def _check(status: int, what: str) -> None:
     if status != FD_OK:
         raise FdError(status, f"{what}: {fd_status_string(status)}: "
                               f"{lib.fd_last_error_message().decode()}")
+
+
+# the compiled marshalling of the serving calls (csrc/binding.cpp), linked to this libfd.so
+if not os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "_fd_binding.so")):
+    raise ImportError("_fd_binding.so is missing beside libfd.so: build it with "
+                      "`python split_kv_decode_flashdecoding_b200/build.py`")
+_fd_binding = importlib.import_module("._fd_binding", __name__)
+_fd_binding.set_raise(_check)
 
 
 # an E4M3 cache may be passed as torch.float8_e4m3fn or as its uint8 codes
@@ -294,82 +303,13 @@ def fd_chunk_prefill_attention(q_chunk: torch.Tensor, k_cache: torch.Tensor,
     return out, lse
 
 
-# The calls below are made once a scheduling step and layer, so their marshalling is kept short: a
-# descriptor is packed in one step, pointers go over as integers, and the device is switched only where
-# it is not the current one.
-_DESC = struct.Struct("=Qii4q4q")
-assert _DESC.size == ctypes.sizeof(FdTensor)
-_PAD = (0, 0, 0, 0)
-
-
-def _desc(t: torch.Tensor) -> bytes:
-    """An fd_tensor of t, as bytes (passed by address)."""
-    shape = t.shape
-    n = len(shape)
-    if n > 4:
-        raise ValueError("at most 4 dimensions")
-    pad = _PAD[n:]
-    return _DESC.pack(t.data_ptr(), _DTYPES.get(t.dtype, -1), n, *shape, *pad, *t.stride(), *pad)
-
-
-def _need(like: torch.Tensor, **tensors: torch.Tensor) -> None:
-    dev = like.device
-    if dev.type != "cuda":
-        raise ValueError(f"CUDA tensors are needed, not {dev.type}")
-    for name, t in tensors.items():
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
-
-
-def _int32(t: torch.Tensor, name: str, dev: torch.device, shape: tuple) -> int:
-    """Address of a contiguous int32 tensor of this shape on the device."""
-    if t.dtype is torch.int32 and t.shape == shape and t.device == dev and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {dev}")
-
-
-# The stream handle without building a torch.cuda.Stream around it (0.1 instead of 2.3 us).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _call(name: str, device: torch.device, stream, *args) -> None:
-    index = device.index
-    if stream is None:
-        raw = _raw_stream(index)
-    else:
-        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if index == torch.cuda.current_device():
-        st = getattr(lib, name)(*args, raw)
-    else:
-        with torch.cuda.device(index):
-            st = getattr(lib, name)(*args, raw)
-    if st != FD_OK:
-        _check(st, name)
-
-
-def _rows_out(q: torch.Tensor, out, lse):
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    if lse is None:
-        lse = q.new_empty(q.shape[:2], dtype=torch.float32)
-    elif lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != q.shape[:2]:
-        raise ValueError("lse must be a contiguous float32 tensor [T, Hq]")
-    return out, lse
-
-
 def fd_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Tensor,
                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                         stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Causal attention of whole prompts packed one after another. q [T,Hq,D]; k, v [T,Hkv,D] (bf16,
     any 16-byte strides of rows and heads); seq_lens int32 [B], summing to at most T. Rows behind
     the last prompt are left as they are. Returns (out [T,Hq,D], lse float32 [T,Hq])."""
-    lens = _int32(seq_lens, "seq_lens", q.device, (seq_lens.numel(),))
-    out, lse = _rows_out(q, out, lse)
-    _need(q, k=k, v=v, out=out, lse=lse)
-    _call("fd_prompt_attention", q.device, stream, _desc(q), _desc(k), _desc(v), lens,
-          seq_lens.numel(), _desc(out), lse.data_ptr())
-    return out, lse
+    return _fd_binding.prompt_attention(q, k, v, seq_lens, out, lse, stream)
 
 
 def fd_prompt_workspace_bytes(batch, total_rows, num_q_heads, num_kv_heads, head_dim) -> int:
@@ -385,15 +325,8 @@ def fd_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     whose keys and values stand in the cache at [prefix_lens[b], prefix_lens[b] + tree_lens[b]);
     draft i sees the prefix and the drafts j with bit j % 32 of tree_mask[row][j // 32] set
     (tree_mask int32 [T, W], W <= 8)."""
-    B = k_cache.shape[0]
-    dev = q.device
-    pre, new = _int32(prefix_lens, "prefix_lens", dev, (B,)), _int32(tree_lens, "tree_lens", dev, (B,))
-    mask = _int32(tree_mask, "tree_mask", dev, (q.shape[0], tree_mask.shape[-1]))
-    out, lse = _rows_out(q, out, lse)
-    _need(q, k_cache=k_cache, v_cache=v_cache, out=out, lse=lse)
-    _call("fd_tree_attention", q.device, stream, _desc(q), _desc(k_cache), _desc(v_cache), pre, new,
-          mask, tree_mask.shape[1], _desc(out), lse.data_ptr())
-    return out, lse
+    return _fd_binding.tree_attention(q, k_cache, v_cache, None, prefix_lens, tree_lens, tree_mask, out, lse,
+                                      stream)
 
 
 def fd_tree_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -404,16 +337,8 @@ def fd_tree_attention_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: tor
                             stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """fd_tree_attention over a paged cache (pages and block_table as in
     fd_decode_attention_paged)."""
-    B, per = block_table.shape
-    table = _int32(block_table, "block_table", q.device, (B, per))
-    dev = q.device
-    pre, new = _int32(prefix_lens, "prefix_lens", dev, (B,)), _int32(tree_lens, "tree_lens", dev, (B,))
-    mask = _int32(tree_mask, "tree_mask", dev, (q.shape[0], tree_mask.shape[-1]))
-    out, lse = _rows_out(q, out, lse)
-    _need(q, k_pages=k_pages, v_pages=v_pages, out=out, lse=lse)
-    _call("fd_tree_attention_paged", q.device, stream, _desc(q), _desc(k_pages), _desc(v_pages),
-          table, per, B, pre, new, mask, tree_mask.shape[1], _desc(out), lse.data_ptr())
-    return out, lse
+    return _fd_binding.tree_attention(q, k_pages, v_pages, block_table, prefix_lens, tree_lens, tree_mask, out,
+                                      lse, stream)
 
 
 def fd_tree_workspace_bytes(batch, total_rows, num_q_heads, num_kv_heads, cache_capacity,
@@ -427,14 +352,7 @@ def fd_pages_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Ten
                     new_lens: torch.Tensor, stream=None) -> None:
     """Write the packed rows k_new, v_new [T,Hkv,D] (new_lens[b] rows a sequence) to the positions
     start_lens[b], start_lens[b] + 1, ... of their sequences' pages (in place)."""
-    dev = k_pages.device
-    B, per = block_table.shape
-    table = _int32(block_table, "block_table", dev, (B, per))
-    start = _int32(start_lens, "start_lens", dev, (B,))
-    new = _int32(new_lens, "new_lens", dev, (B,))
-    _need(k_pages, k_new=k_new, v_new=v_new, v_pages=v_pages)
-    _call("fd_pages_append", k_pages.device, stream, _desc(k_new), _desc(v_new), _desc(k_pages),
-          _desc(v_pages), table, per, B, start, new)
+    _fd_binding.pages_append(k_new, v_new, k_pages, v_pages, None, None, block_table, start_lens, new_lens, stream)
 
 
 def fd_pages_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor,
@@ -443,28 +361,15 @@ def fd_pages_append_fp8(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch
                         new_lens: torch.Tensor, stream=None) -> None:
     """fd_pages_append into E4M3 pages (float8_e4m3fn, or uint8 codes): the code of x is the E4M3
     value nearest to x / scale."""
-    dev = k_pages.device
-    B, per = block_table.shape
-    table = _int32(block_table, "block_table", dev, (B, per))
-    start = _int32(start_lens, "start_lens", dev, (B,))
-    new = _int32(new_lens, "new_lens", dev, (B,))
-    _need(k_pages, k_new=k_new, v_new=v_new, v_pages=v_pages)
-    _call("fd_pages_append_fp8", k_pages.device, stream, _desc(k_new), _desc(v_new),
-          _desc(k_pages), _desc(v_pages), float(k_scale), float(v_scale), table, per, B, start, new)
+    _fd_binding.pages_append(k_new, v_new, k_pages, v_pages, k_scale, v_scale, block_table, start_lens, new_lens,
+                             stream)
 
 
 def fd_pages_reserve(page_refs: torch.Tensor, block_table: torch.Tensor, want_lens: torch.Tensor,
                      page_size: int, stream=None) -> None:
     """Give every sequence the pages for want_lens[b] tokens: free ones (page_refs 0), lowest
     index first, in the order of the sequences (block_table and page_refs in place)."""
-    dev = page_refs.device
-    refs = _int32(page_refs, "page_refs", dev, (page_refs.numel(),))
-    B, per = block_table.shape
-    table = _int32(block_table, "block_table", dev, (B, per))
-    want = _int32(want_lens, "want_lens", dev, (B,))
-    _need(page_refs)
-    _call("fd_pages_reserve", page_refs.device, stream, refs, page_refs.numel(), table, per, B, want,
-          int(page_size))
+    _fd_binding.pages_reserve(page_refs, block_table, want_lens, page_size, stream)
 
 
 def fd_pages_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_refs: torch.Tensor,
@@ -472,31 +377,13 @@ def fd_pages_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_refs: torch
                   dst_seqs: torch.Tensor, stream=None) -> None:
     """Make the empty sequence dst_seqs[i] a copy of src_seqs[i]: full pages are shared, the rows
     of a last, partly filled page are copied to a new page (all state in place)."""
-    dev = k_pages.device
-    refs = _int32(page_refs, "page_refs", dev, (k_pages.shape[0],))
-    B, per = block_table.shape
-    table = _int32(block_table, "block_table", dev, (B, per))
-    lens = _int32(cache_lens, "cache_lens", dev, (B,))
-    count = src_seqs.numel()
-    src = _int32(src_seqs, "src_seqs", dev, (count,))
-    dst = _int32(dst_seqs, "dst_seqs", dev, (count,))
-    _need(k_pages, v_pages=v_pages)
-    _call("fd_pages_fork", k_pages.device, stream, _desc(k_pages), _desc(v_pages), refs, table, per,
-          B, lens, src, dst, count)
+    _fd_binding.pages_fork(k_pages, v_pages, page_refs, block_table, cache_lens, src_seqs, dst_seqs, stream)
 
 
 def fd_pages_free(page_refs: torch.Tensor, block_table: torch.Tensor, cache_lens: torch.Tensor,
                   seqs: torch.Tensor, stream=None) -> None:
     """Empty the rows of the listed sequences and give their references back (in place)."""
-    dev = page_refs.device
-    refs = _int32(page_refs, "page_refs", dev, (page_refs.numel(),))
-    B, per = block_table.shape
-    table = _int32(block_table, "block_table", dev, (B, per))
-    lens = _int32(cache_lens, "cache_lens", dev, (B,))
-    ids = _int32(seqs, "seqs", dev, (seqs.numel(),))
-    _need(page_refs)
-    _call("fd_pages_free", page_refs.device, stream, refs, page_refs.numel(), table, per, B, lens,
-          ids, seqs.numel())
+    _fd_binding.pages_free(page_refs, block_table, cache_lens, seqs, stream)
 
 
 def fd_pages_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_refs: torch.Tensor,
@@ -506,17 +393,7 @@ def fd_pages_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_refs: to
     """Keep the tokens start_lens[b] + keep[b, :keep_lens[b]] of every sequence with keep_lens[b] >= 0,
     moved to start_lens[b], start_lens[b] + 1, ...; cache_lens and the pages follow (in place).
     keep int32 [B, max_keep], strictly increasing rows."""
-    dev = k_pages.device
-    refs = _int32(page_refs, "page_refs", dev, (k_pages.shape[0],))
-    B, per = block_table.shape
-    table = _int32(block_table, "block_table", dev, (B, per))
-    lens = _int32(cache_lens, "cache_lens", dev, (B,))
-    start = _int32(start_lens, "start_lens", dev, (B,))
-    kept = _int32(keep_lens, "keep_lens", dev, (B,))
-    lists = _int32(keep, "keep", dev, (B, keep.shape[-1]))
-    _need(k_pages, v_pages=v_pages)
-    _call("fd_pages_compact", k_pages.device, stream, _desc(k_pages), _desc(v_pages), refs, table,
-          per, B, lens, start, lists, keep.shape[1], kept)
+    _fd_binding.pages_compact(k_pages, v_pages, page_refs, block_table, cache_lens, start_lens, keep, keep_lens, stream)
 
 
 def fd_split_plan(cache_lens: Sequence[int], num_kv_heads: int, cache_capacity: int,

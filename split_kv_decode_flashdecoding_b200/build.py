@@ -1,27 +1,32 @@
-"""Build the C-ABI library libfd.so in-tree with nvcc for sm_100a.
+"""Build the C-ABI library libfd.so (nvcc, sm_100a) and the Python binding's module in-tree.
 
 Usage: python split_kv_decode_flashdecoding_b200/build.py [--force] [-v]
 (run by path: importing the package needs the library already built)
 
 The CUDA runtime is linked statically and the driver entry points the library needs are
 fetched at run time, so the library loads on a machine without a GPU driver (its attention
-calls then fail with FD_ERR_CUDA) and needs nothing but the driver on a GPU machine.
+calls then fail with FD_ERR_CUDA) and needs nothing but the driver on a GPU machine. The module
+(csrc/binding.cpp) marshals the serving calls' tensors for libfd.so and is linked to torch.
 """
 
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfd.so")
+BINDING = os.path.join(PKG, "_fd_binding.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -47,11 +52,12 @@ def _deps():
     return deps
 
 
+def _newer(target: str, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(d) <= os.path.getmtime(target) for d in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _newer(LIB, _deps())
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -67,9 +73,38 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch not found: the binding is built against it")
+    return list(spec.submodule_search_locations)[0]
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp against torch and libfd.so (which has to be there); returns its path."""
+    if not force and _newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "fd.h")]):
+        return BINDING
+    torch_dir, cuda = _torch_dir(), os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cxx = shutil.which("g++") or "c++"
+    tmp = BINDING + ".tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           *(x for d in (os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"))
+             for x in ("-isystem", d)),
+           "-I", INCLUDE, BINDING_SRC, "-o", tmp, "-L", PKG, "-l:libfd.so", "-L", os.path.join(torch_dir, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-l:libstdc++.so.6", "-Wl,-rpath,$ORIGIN"]  # the libstdc++ that torch uses, by name
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu under csrc/ and link libfd.so; returns its path."""
+    """Compile every .cu under csrc/, link libfd.so and build the binding's module; returns
+    libfd.so's path."""
     if not force and up_to_date():
+        build_binding()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
@@ -81,6 +116,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding(force)
     return LIB
 
 

@@ -245,3 +245,26 @@ def test_capacities_near_2_to_the_31_are_refused():
         return fd.lib.fd_tree_attention_paged(_ref(q), _ref(kv), _ref(kv), _i(), pages, 1, _i(), _i(), _i(), 1, _ref(q), _f(), None)
 
     assert tree((2**31 - 1024) // 8 + 1, 8) == UNS and tree(2**31 // 128 - 1, 128) == UNS
+
+
+def test_binding_names_what_it_refuses():
+    q, n = torch.zeros(4, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
+    pages, table = torch.zeros(3, 1, 8, 64, dtype=torch.bfloat16), torch.zeros(1, 3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA tensors are needed, not cpu"):
+        fd.fd_prompt_attention(q, q, q, n)
+    with pytest.raises(ValueError, match="seq_lens must be a contiguous int32 tensor"):
+        fd.fd_prompt_attention(q, q, q, n.float())
+    with pytest.raises(ValueError, match=r"q must be \[T, Hq, D\]"):
+        fd.fd_prompt_attention(q[0], q, q, n)
+    with pytest.raises(ValueError, match=r"block_table must be \[B, pages_per_seq\]"):
+        fd.fd_pages_reserve(n, n, n, 16)
+    with pytest.raises(ValueError, match="page_size is out of range"):
+        fd.fd_pages_reserve(n, table, n, 2**31)
+    with pytest.raises(ValueError, match="tree_mask must be a contiguous int32 tensor"):
+        fd.fd_tree_attention_paged(q, pages, pages, table, n, n, torch.zeros(3, 1, dtype=torch.int32))
+    with pytest.raises(TypeError, match="v must be a tensor"):
+        fd.fd_prompt_attention(q, q, None, n)
+    with pytest.raises(TypeError):
+        fd.fd_pages_reserve(n, table, n, 1.5)
+    with pytest.raises(TypeError):
+        fd.fd_pages_append_fp8(q, q, pages, pages, "1", 1.0, table, n, n)
