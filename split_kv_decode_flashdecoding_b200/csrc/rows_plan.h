@@ -57,12 +57,13 @@ FD_HD int32_t rows_active(int64_t weight, int64_t items, int32_t nctas) {
 
 // The line cut into stretches, of `share` units each and one more in the first `rest`. Dividing 64-bit
 // integers is a subroutine of ~100 dependent instructions, and a CTA looks at some twenty bounds before
-// its first load: one division here, in doubles, none below.
+// its first load: one division here, of 32-bit integers or in doubles, none below.
 struct RowsLine {
   int64_t share;
   int32_t rest, nact;
 };
 FD_HD int64_t rows_quotient(int64_t x, int64_t d) {  // floor(x / d), x >= 0, d > 0
+  if (((x | d) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
   int64_t q = static_cast<int64_t>(static_cast<double>(x) / static_cast<double>(d));
   while (q * d > x) --q;
   while ((q + 1) * d <= x) ++q;
