@@ -156,20 +156,22 @@ __device__ __forceinline__ void append_load(AppendUnit<S, kFp8>& a, const S* src
 
 // x / s rounded to fp32 as the division rounds it: one Newton step on x times the rounded reciprocal r
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), for s
-// with a normal reciprocal. Quotients far beyond the largest code (and infinities, whose step would be
-// NaN) stay as the product gives them.
+// with a normal reciprocal. A zero's sign may be lost. Not for quotients near overflow, whose step would
+// be NaN: those above 1e6 stay as the product gives them.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = x * r;
-  const float d = copysignf(fmaf(fmaf(-q, s, x), r, q), q);  // -0 keeps its sign
-  return fabsf(q) < 1e6f ? d : q;
+  return fabsf(q) < 1e6f ? fmaf(fmaf(-q, s, x), r, q) : q;
 }
 
+// E4M3 codes of 16 values' magnitudes x / s under the signs of the values (s > 0), which stand in the
+// upper bits of their words. Two quotients an instruction; the test for large ones is made once for all.
 template <typename S, bool kFp8>
 __device__ __forceinline__ uint4 append_convert(const AppendUnit<S, kFp8>& a, float scale, float recip) {
   if constexpr (!kFp8) {
     return a.v[0];
   } else {
     float x[16];
+    uint32_t sign[4];  // of values 4 i .. 4 i + 3, in the bytes' upper bits
 #pragma unroll
     for (int i = 0; i < AppendUnit<S, kFp8>::kLoads; ++i) {
       const uint32_t w[4] = {a.v[i].x, a.v[i].y, a.v[i].z, a.v[i].w};
@@ -182,10 +184,33 @@ __device__ __forceinline__ uint4 append_convert(const AppendUnit<S, kFp8>& a, fl
           x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
         }
       }
+      if constexpr (sizeof(S) == 4) {
+        sign[i] = __byte_perm(__byte_perm(w[0], w[1], 0x0073), __byte_perm(w[2], w[3], 0x0073), 0x5410);
+      } else {
+        sign[2 * i] = __byte_perm(w[0], w[1], 0x7531);
+        sign[2 * i + 1] = __byte_perm(w[2], w[3], 0x7531);
+      }
     }
-    // a scale without a normal reciprocal (recip 0) divides
+    uint64_t q[8];
+    const uint64_t r2 = pair_f32(recip, recip), s2 = pair_f32(-scale, -scale);
+    float most = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = recip != 0.f ? quotient(x[i], scale, recip) : __fdiv_rn(x[i], scale);
+    for (int i = 0; i < 8; ++i) {
+      q[i] = fma_f32x2(pair_f32(x[2 * i], x[2 * i + 1]), r2, 0ull);
+      float lo, hi;
+      unpair_f32(q[i], lo, hi);
+      most = fmaxf(most, fmaxf(fabsf(lo), fabsf(hi)));
+    }
+    if (recip != 0.f && most < 1e6f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t rest = fma_f32x2(q[i], s2, pair_f32(x[2 * i], x[2 * i + 1]));
+        unpair_f32(fma_f32x2(rest, r2, q[i]), x[2 * i], x[2 * i + 1]);
+      }
+    } else {  // a large value, or a scale without a normal reciprocal (recip 0)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = recip != 0.f ? quotient(x[i], scale, recip) : __fdiv_rn(x[i], scale);
+    }
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -195,6 +220,7 @@ __device__ __forceinline__ uint4 append_convert(const AppendUnit<S, kFp8>& a, fl
           "mov.b32 %0, {lo, hi};\n\t}"
           : "=r"(o[i])
           : "f"(x[4 * i]), "f"(x[4 * i + 1]), "f"(x[4 * i + 2]), "f"(x[4 * i + 3]));
+      o[i] = (o[i] & 0x7f7f7f7fu) | (sign[i] & 0x80808080u);
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
   }
@@ -205,7 +231,7 @@ __device__ __forceinline__ uint4 append_convert(const AppendUnit<S, kFp8>& a, fl
 // and V, in 16-byte units of the destination, four a lane in flight. Bound by HBM; E4M3 from bf16 by the
 // conversion's instructions as well (~8 a value).
 template <typename S, bool kFp8>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p) {
   extern __shared__ int64_t s_end[];  // [batch] ends of the sequences' packed rows
   __shared__ int64_t s_warp[kAppendThreads / 32];
   __shared__ int64_t s_place[kAppendRows];  // element offset of the row's place in both pools, < 0: none
@@ -402,15 +428,21 @@ __global__ void __launch_bounds__(kTableThreads) fork_plan_kernel(const ForkPara
     if (dst >= 0 && dst < p.batch) atomicMin(&s_owner[dst], i);
   }
   __syncthreads();
-  for (int i = warp; i < p.count; i += kTableThreads / 32) {
+  // the indices and lengths, a thread a pair; then the sources' pages, a warp a pair
+  for (int i = threadIdx.x; i < p.count; i += kTableThreads) {
     const int src = p.src_seqs[i], dst = p.dst_seqs[i];
-    int len = -1;
+    const bool ok = src >= 0 && src < p.batch && dst >= 0 && dst < p.batch && s_owner[dst] == i &&
+                    p.block_table[static_cast<int64_t>(dst) * p.pages_per_seq] < 0;
+    if (!ok) atomicOr(p.status, FD_FLAG_BAD_INDEX);
+    s_sum[i] = ok ? 1 : 0;
+    s_len[i] = ok ? p.cache_lens[src] : -1;
+  }
+  __syncthreads();
+  for (int i = warp; i < p.count; i += kTableThreads / 32) {
+    const int src = p.src_seqs[i];
+    int len = s_len[i];
     uint32_t flag = 0;
-    if (src < 0 || src >= p.batch || dst < 0 || dst >= p.batch || s_owner[dst] != i ||
-        p.block_table[static_cast<int64_t>(dst) * p.pages_per_seq] >= 0) {
-      flag = FD_FLAG_BAD_INDEX;
-    } else {
-      len = p.cache_lens[src];
+    if (s_sum[i] != 0) {
       const int64_t pages = (static_cast<int64_t>(len) + p.page_size - 1) / p.page_size;
       bool ok = len >= 0 && pages <= p.pages_per_seq;
       const int32_t* row = p.block_table + static_cast<int64_t>(src) * p.pages_per_seq;
@@ -433,6 +465,7 @@ __global__ void __launch_bounds__(kTableThreads) fork_plan_kernel(const ForkPara
         flag = FD_FLAG_BAD_PAGE;
       }
     }
+    __syncwarp();  // s_len and s_sum are read
     if (lane == 0) {
       if (flag) atomicOr(p.status, flag);
       s_len[i] = len;
@@ -588,8 +621,9 @@ __device__ __forceinline__ bool check_compact(const CompactParams& p, int b, int
 // thread after the other. The list increases strictly, so a row read lies at or behind the row written for
 // it: rows read for a later batch lie behind every row written for an earlier one. A batch's rows are
 // therefore loaded before the batch before it is stored, and only a batch's own loads and stores need the
-// barrier between them. The places of a batch are looked up two or three batches ahead, one
-// thread a row, in a ring of four.
+// barrier between them. The places of a batch are looked up one thread a row, in a ring of four: its
+// list entries four batches ahead, its pages three, both waited for a batch later, so that a batch costs one
+// memory latency and not the lookup's two behind each other.
 constexpr int kMove = 8;
 constexpr int kMoveRows = kMove * kCompactThreads / 4;  // rows of a batch at most (64-byte rows)
 __global__ void __launch_bounds__(kCompactThreads) compact_move_kernel(const CompactParams p) {
@@ -610,17 +644,34 @@ __global__ void __launch_bounds__(kCompactThreads) compact_move_kernel(const Com
   const int32_t start = p.start_lens[b];
   const int32_t* keep = p.keep + static_cast<int64_t>(b) * p.max_keep;
   const int32_t* row = p.block_table + static_cast<int64_t>(b) * p.pages_per_seq;
-  auto at = [&](int pos) {
-    return row[pos / p.page_size] * p.pool_sp + static_cast<int64_t>(pos % p.page_size) * p.row_bytes;
-  };
-  auto look_up = [&](int n) {  // the places of batch n
-    for (int k = tid; k < batch; k += kCompactThreads) {
-      const int i = first + n * batch + k;
-      if (i < m) {
-        s_from[n & 3][k] = at(start + keep[i]);
-        s_to[n & 3][k] = at(start + i);
-      }
+  // lookups in flight: of the batch whose list entries are read, and of the one whose pages are
+  constexpr int kLook = kMoveRows / kCompactThreads;
+  int entry[kLook], pos[kLook], page_from[kLook], page_to[kLook];
+  auto each = [&](int n, auto f) {
+#pragma unroll
+    for (int k = 0; k < kLook; ++k) {
+      const int at = k * kCompactThreads + tid, i = first + n * batch + at;
+      if (at < batch && i < m) f(k, at, i);
     }
+  };
+  auto read_list = [&](int n) { each(n, [&](int k, int, int i) { entry[k] = keep[i]; }); };
+  auto read_pages = [&](int n) {
+    each(n, [&](int k, int, int i) {
+      pos[k] = start + entry[k];
+      page_from[k] = row[pos[k] / p.page_size];
+      page_to[k] = row[(start + i) / p.page_size];
+    });
+  };
+  auto put_places = [&](int n) {
+    each(n, [&](int k, int at, int i) {
+      s_from[n & 3][at] = page_from[k] * p.pool_sp + static_cast<int64_t>(pos[k] % p.page_size) * p.row_bytes;
+      s_to[n & 3][at] = page_to[k] * p.pool_sp + static_cast<int64_t>((start + i) % p.page_size) * p.row_bytes;
+    });
+  };
+  auto look_up = [&](int n) {  // the places of batch n, and what the next two need
+    put_places(n);
+    read_pages(n + 1);
+    read_list(n + 2);
   };
   auto load = [&](int n, uint4 (&x)[kMove]) {
 #pragma unroll
@@ -635,19 +686,22 @@ __global__ void __launch_bounds__(kCompactThreads) compact_move_kernel(const Com
   };
   const int batches = (m - first + batch - 1) / batch;
   uint4 x[kMove], y[kMove];
+  read_list(0);
+  read_pages(0);
+  read_list(1);
   look_up(0);
-  if (batches > 1) look_up(1);
+  look_up(1);
   __syncthreads();
   load(0, x);
   // two batches a round, so that the registers keep their roles
   for (int n = 0; n < batches; n += 2) {
     if (n + 1 < batches) load(n + 1, y);
-    if (n + 2 < batches) look_up(n + 2);
+    look_up(n + 2);
     __syncthreads();  // everyone has loaded batch n (and n + 1)
     store(n, x);
     if (n + 1 >= batches) break;
     if (n + 2 < batches) load(n + 2, x);
-    if (n + 3 < batches) look_up(n + 3);
+    look_up(n + 3);
     __syncthreads();
     store(n + 1, y);
   }

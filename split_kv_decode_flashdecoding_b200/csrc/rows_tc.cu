@@ -102,26 +102,6 @@ static_assert(sizeof(RwSmem<128, false>) + 1024 <= 227 * 1024, "row attention sh
 static_assert(sizeof(RwSmem<64, true>) + 1024 <= 227 * 1024, "row attention shared memory");
 static_assert(sizeof(RwSmem<64, false>) + 1024 <= 227 * 1024, "row attention shared memory");
 
-// ---- arithmetic on pairs of fp32 ------------------------------------------------------------------
-
-__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair_f32(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // Maximum that a NaN wins, so that a row which sees one becomes NaN as a whole.
 __device__ __forceinline__ float max3_f32(float a, float b, float c) {
   float r;
