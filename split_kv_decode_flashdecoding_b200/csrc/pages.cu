@@ -327,9 +327,10 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendP
 
 constexpr int kRowsAtOnce = 4;
 
-// One CTA. A warp counts the pages of four sequences at a time; the missing ones, summed over the sequences, are the
-// ranks of the free pages that visit_free_pages gives. If they run out, the sequences whose sum
-// exceeds what there was give back what they got.
+// One CTA. A warp counts the pages of one sequence, or of four at a time where there are more sequences than
+// warps; the missing ones, summed over the sequences, are the ranks of the free pages that
+// visit_free_pages gives. If they run out, the sequences whose sum exceeds what there was give back what
+// they got. Bound by the latency of its dependent loads (the rows, the references).
 __global__ void __launch_bounds__(kTableThreads) reserve_kernel(const ReserveParams p) {
   extern __shared__ int64_t s_sum[];  // [batch] inclusive sums of the missing pages
   int32_t* s_have = reinterpret_cast<int32_t*>(s_sum + p.batch);
@@ -349,40 +350,51 @@ __global__ void __launch_bounds__(kTableThreads) reserve_kernel(const ReservePar
     s_sum[b] = want;
   }
   __syncthreads();
-  for (int b0 = warp * kRowsAtOnce; b0 < p.batch; b0 += kTableThreads / 32 * kRowsAtOnce) {
-    int most = 0, limit[kRowsAtOnce];
-#pragma unroll
-    for (int i = 0; i < kRowsAtOnce; ++i) {
-      limit[i] = b0 + i < p.batch ? s_have[b0 + i] : 0;
-      most = max(most, limit[i]);
-    }
-    int have[kRowsAtOnce];
-#pragma unroll
-    for (int i = 0; i < kRowsAtOnce; ++i) have[i] = limit[i];
-    for (int c0 = 0; c0 < most; c0 += 64) {
-      int32_t e[kRowsAtOnce][2];
-#pragma unroll
-      for (int i = 0; i < kRowsAtOnce; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int c = c0 + 32 * k + lane;
-          e[i][k] = c < limit[i] ? p.block_table[static_cast<int64_t>(b0 + i) * p.pages_per_seq + c] : 0;
-        }
-#pragma unroll
-      for (int i = 0; i < kRowsAtOnce; ++i)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const unsigned neg = __ballot_sync(0xffffffffu, e[i][k] < 0);
-          if (neg) have[i] = min(have[i], c0 + 32 * k + __ffs(neg) - 1);
-        }
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kRowsAtOnce; ++i)
-      if (lane == 0 && b0 + i < p.batch) {
-        s_have[b0 + i] = have[i];
-        s_sum[b0 + i] -= have[i];
+  if (p.batch <= kTableThreads / 32) {  // a warp for every row
+    if (warp < p.batch) {
+      const int have = leading_pages(p.block_table + static_cast<int64_t>(warp) * p.pages_per_seq, s_have[warp]);
+      __syncwarp();
+      if (lane == 0) {
+        s_have[warp] = have;
+        s_sum[warp] -= have;
       }
+    }
+  } else {
+    for (int b0 = warp * kRowsAtOnce; b0 < p.batch; b0 += kTableThreads / 32 * kRowsAtOnce) {
+      int most = 0, limit[kRowsAtOnce];
+#pragma unroll
+      for (int i = 0; i < kRowsAtOnce; ++i) {
+        limit[i] = b0 + i < p.batch ? s_have[b0 + i] : 0;
+        most = max(most, limit[i]);
+      }
+      int have[kRowsAtOnce];
+#pragma unroll
+      for (int i = 0; i < kRowsAtOnce; ++i) have[i] = limit[i];
+      for (int c0 = 0; c0 < most; c0 += 64) {
+        int32_t e[kRowsAtOnce][2];
+#pragma unroll
+        for (int i = 0; i < kRowsAtOnce; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int c = c0 + 32 * k + lane;
+            e[i][k] = c < limit[i] ? p.block_table[static_cast<int64_t>(b0 + i) * p.pages_per_seq + c] : 0;
+          }
+#pragma unroll
+        for (int i = 0; i < kRowsAtOnce; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const unsigned neg = __ballot_sync(0xffffffffu, e[i][k] < 0);
+            if (neg) have[i] = min(have[i], c0 + 32 * k + __ffs(neg) - 1);
+          }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kRowsAtOnce; ++i)
+        if (lane == 0 && b0 + i < p.batch) {
+          s_have[b0 + i] = have[i];
+          s_sum[b0 + i] -= have[i];
+        }
+    }
   }
   __syncthreads();
   const int64_t need = scan_array(s_sum, p.batch, s_warp);
