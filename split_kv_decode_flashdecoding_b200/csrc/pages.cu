@@ -435,26 +435,24 @@ __global__ void __launch_bounds__(kTableThreads) fork_plan_kernel(const ForkPara
   pdl_wait_prerequisites();
   for (int b = threadIdx.x; b < p.batch; b += kTableThreads) s_owner[b] = INT32_MAX;
   __syncthreads();
-  for (int i = threadIdx.x; i < p.count; i += kTableThreads) {
-    const int dst = p.dst_seqs[i];
-    if (dst >= 0 && dst < p.batch) atomicMin(&s_owner[dst], i);
-  }
-  __syncthreads();
   // the indices and lengths, a thread a pair; then the sources' pages, a warp a pair
   for (int i = threadIdx.x; i < p.count; i += kTableThreads) {
     const int src = p.src_seqs[i], dst = p.dst_seqs[i];
-    const bool ok = src >= 0 && src < p.batch && dst >= 0 && dst < p.batch && s_owner[dst] == i &&
-                    p.block_table[static_cast<int64_t>(dst) * p.pages_per_seq] < 0;
-    if (!ok) atomicOr(p.status, FD_FLAG_BAD_INDEX);
-    s_sum[i] = ok ? 1 : 0;
+    bool ok = dst >= 0 && dst < p.batch;
+    if (ok) atomicMin(&s_owner[dst], i);
+    ok = ok && src >= 0 && src < p.batch;
     s_len[i] = ok ? p.cache_lens[src] : -1;
+    s_sum[i] = ok && p.block_table[static_cast<int64_t>(dst) * p.pages_per_seq] < 0 ? 1 : 0;
   }
   __syncthreads();
   for (int i = warp; i < p.count; i += kTableThreads / 32) {
-    const int src = p.src_seqs[i];
-    int len = s_len[i];
+    const int src = p.src_seqs[i], dst = p.dst_seqs[i];
+    int len = -1;
     uint32_t flag = 0;
-    if (s_sum[i] != 0) {
+    if (s_sum[i] == 0 || s_owner[dst] != i) {
+      flag = FD_FLAG_BAD_INDEX;
+    } else {
+      len = s_len[i];
       const int64_t pages = (static_cast<int64_t>(len) + p.page_size - 1) / p.page_size;
       bool ok = len >= 0 && pages <= p.pages_per_seq;
       const int32_t* row = p.block_table + static_cast<int64_t>(src) * p.pages_per_seq;
