@@ -137,7 +137,7 @@ __device__ __forceinline__ int64_t scan_array(int64_t* s, int n, int64_t* s_warp
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendRows = 32;  // rows whose places one CTA looks up together
-// Units a lane has in flight. E4M3 from bf16: two keep 4 CTAs resident (four: 97 registers, 2 CTAs).
+// Units a lane has in flight. E4M3: two, whose 64 registers keep 4 CTAs resident (four: 97, 2 CTAs).
 template <bool kFp8>
 constexpr int kAppendUnits = kFp8 ? 2 : 4;
 
@@ -228,8 +228,10 @@ __device__ __forceinline__ uint4 append_convert(const AppendUnit<S, kFp8>& a, fl
 
 // A CTA takes p.rows_per_cta packed rows. Every thread sums new_lens (the ends of the sequences,
 // shared memory); one thread a row finds the row's sequence, page and slot; then a warp takes a row, K
-// and V, in 16-byte units of the destination, four a lane in flight. Bound by HBM; E4M3 from bf16 by the
-// conversion's instructions as well (~8 a value).
+// and V, in 16-byte units of the destination, two or four a lane in flight. Bound by HBM: 65,536 bf16 rows
+// of 8 heads of 128 in 82 us (537 MB, 6.5 TB/s); E4M3 from bf16 by the conversion's instructions as well
+// (~4 a value): 65,005 rows in 74 us (399 MB, 5.4 TB/s; 95 us with ~8 a value). One token of each of 64
+// sequences: 3.7 us, three dependent loads and the launch.
 template <typename S, bool kFp8>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const AppendParams p) {
   extern __shared__ int64_t s_end[];  // [batch] ends of the sequences' packed rows
@@ -330,7 +332,8 @@ constexpr int kRowsAtOnce = 4;
 // One CTA. A warp counts the pages of one sequence, or of four at a time where there are more sequences than
 // warps; the missing ones, summed over the sequences, are the ranks of the free pages that
 // visit_free_pages gives. If they run out, the sequences whose sum exceeds what there was give back what
-// they got. Bound by the latency of its dependent loads (the rows, the references).
+// they got. Bound by the latency of its dependent loads (the rows, the references): a step of 32 sequences
+// of up to 415 pages took 2.1 us longer with four rows a warp.
 __global__ void __launch_bounds__(kTableThreads) reserve_kernel(const ReserveParams p) {
   extern __shared__ int64_t s_sum[];  // [batch] inclusive sums of the missing pages
   int32_t* s_have = reinterpret_cast<int32_t*>(s_sum + p.batch);
@@ -422,7 +425,8 @@ __global__ void __launch_bounds__(kTableThreads) reserve_kernel(const ReservePar
 // ---- fork -----------------------------------------------------------------------------------------
 
 // One CTA plans the pairs: checks, new pages, rows and references; the copies of the last pages'
-// rows (p.copies) are fork_copy_kernel's.
+// rows (p.copies) are fork_copy_kernel's. Bound by the latency of its dependent loads: 16 pairs 11 us, 96
+// pairs of up to 118 pages 22 us from a cold cache.
 __global__ void __launch_bounds__(kTableThreads) fork_plan_kernel(const ForkParams p) {
   extern __shared__ int64_t s_sum[];  // [count] inclusive sums of the new pages
   int32_t* s_len = reinterpret_cast<int32_t*>(s_sum + p.count);  // [count] tokens, -1: skipped
@@ -523,7 +527,8 @@ __global__ void __launch_bounds__(kTableThreads) fork_plan_kernel(const ForkPara
 
 constexpr int kCopyThreads = 256;
 
-// Block (i, j): the K (j even) or V rows of KV head j / 2 of copy i, contiguous in both pages.
+// Block (i, j): the K (j even) or V rows of KV head j / 2 of copy i, contiguous in both pages. 96 copies of
+// up to 127 rows of 8 heads of 128 bf16: 9 us from a cold cache (51 MB).
 __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const ForkParams p) {
   pdl_launch_dependents();
   pdl_wait_prerequisites();
@@ -549,7 +554,7 @@ __global__ void __launch_bounds__(kCopyThreads) fork_copy_kernel(const ForkParam
 
 constexpr int kFreeThreads = 128;
 
-// One CTA a listed sequence; the first of equal entries frees it.
+// One CTA a listed sequence; the first of equal entries frees it. 4 us for 16 to 96 sequences: latency.
 __global__ void __launch_bounds__(kFreeThreads) free_kernel(const FreeParams p) {
   const int i = blockIdx.x, tid = threadIdx.x;
   pdl_launch_dependents();
@@ -633,7 +638,8 @@ __device__ __forceinline__ bool check_compact(const CompactParams& p, int b, int
 // therefore loaded before the batch before it is stored, and only a batch's own loads and stores need the
 // barrier between them. The places of a batch are looked up one thread a row, in a ring of four: its
 // list entries four batches ahead, its pages three, both waited for a batch later, so that a batch costs one
-// memory latency and not the lookup's two behind each other.
+// memory latency and not the lookup's two behind each other: half of 16 x 4096 tokens (8 heads of 128
+// bf16, 268 MB) in 53 us, 5.1 TB/s, instead of 79.
 constexpr int kMove = 8;
 constexpr int kMoveRows = kMove * kCompactThreads / 4;  // rows of a batch at most (64-byte rows)
 __global__ void __launch_bounds__(kCompactThreads) compact_move_kernel(const CompactParams p) {
