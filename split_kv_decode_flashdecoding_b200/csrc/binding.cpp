@@ -1,7 +1,8 @@
 // Argument marshalling of the serving calls (prompt and tree attention, page operators) for the Python
 // package: a CPython module over the C ABI of include/fd.h. These calls are made once a scheduling
-// step and layer, and on short batches the host is what they wait for: through ctypes a page call
-// took 9-11 us of host time, of which the library and the launch take 3.
+// step and layer, and on short batches the host is what they wait for: through ctypes an append took
+// 10.7 us of host time and a prompt or tree call 16 to 18, here 3.5 to 5.1 and 6 to 9 (the kernels: 3.7 and
+// 10 to 13).
 #include <Python.h>
 
 #include <ATen/Functions.h>
@@ -47,6 +48,7 @@ int32_t* int32s(PyObject* o, const char* name, c10::Device dev, at::IntArrayRef 
   const at::Tensor& t = tensor(o, name);
   TORCH_CHECK_VALUE(t.scalar_type() == at::kInt && t.sizes() == shape && t.device() == dev && t.is_contiguous(),
                     name, " must be a contiguous int32 tensor ", shape, " on ", dev);
+  for (const int64_t n : shape) TORCH_CHECK_VALUE(n <= std::numeric_limits<int32_t>::max(), name, " has 2^31 or more entries");
   return static_cast<int32_t*>(t.data_ptr());
 }
 
