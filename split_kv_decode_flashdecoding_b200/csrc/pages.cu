@@ -7,6 +7,7 @@
 #include "abi_internal.h"
 #include "common.cuh"
 #include "pages.h"
+#include "pairs.cuh"
 
 namespace fd {
 
