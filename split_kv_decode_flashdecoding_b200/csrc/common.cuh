@@ -384,6 +384,19 @@ __device__ __forceinline__ void pdl_wait_prerequisites() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// ---- launches with a variable amount of dynamic shared memory ------------------------------------
+
+// Lets `kernel` be launched with `smem` bytes. Without this, dynamic and static shared memory together
+// may take 48 KB (the kernels that use it hold less than 16 KB of static). The limit is the kernel's, not
+// the launch's, so it is always raised to the same `most` bytes: another thread that launches with a
+// smaller size then cannot lower it between this call and the launch.
+template <typename K>
+inline cudaError_t allow_dynamic_smem(K* kernel, size_t smem, size_t most) {
+  if (smem <= 32 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(most));
+}
+
 // ---- numerics -------------------------------------------------------------------------------
 
 // 2^x with the hardware approximation (relative error ~2^-22); ex2(-inf) = 0.

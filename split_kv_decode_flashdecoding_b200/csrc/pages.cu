@@ -754,13 +754,11 @@ __global__ void __launch_bounds__(kFreeThreads) compact_table_kernel(const Compa
 
 // Launched with programmatic stream serialization: a kernel becomes resident while the one before it
 // runs, and waits for it before it reads or writes anything.
+// `most`: the dynamic shared memory of the largest call, `smem` that of this one.
 template <typename P>
-static cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+static cudaError_t launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, size_t most, cudaStream_t stream, const P& p) {
+  const cudaError_t e = allow_dynamic_smem(kernel, smem, most);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -781,28 +779,31 @@ cudaError_t launch_append(AppendParams p, int src_dtype, bool fp8, int nsm, cuda
   if (grid > 16 * nsm) grid = 16 * nsm;
   void (*kernel)(AppendParams) = src_dtype == FD_F32 ? (fp8 ? append_kernel<float, true> : append_kernel<float, false>)
                                                      : (fp8 ? append_kernel<__nv_bfloat16, true> : append_kernel<__nv_bfloat16, false>);
-  return launch(kernel, dim3(static_cast<unsigned>(grid)), kAppendThreads, sizeof(int64_t) * p.batch, stream, p);
+  return launch(kernel, dim3(static_cast<unsigned>(grid)), kAppendThreads, sizeof(int64_t) * p.batch,
+                sizeof(int64_t) * kMaxPlanBatch, stream, p);
 }
 
 cudaError_t launch_reserve(const ReserveParams& p, cudaStream_t stream) {
-  return launch(reserve_kernel, dim3(1), kTableThreads, static_cast<size_t>(p.batch) * 12, stream, p);
+  const auto smem = [](int32_t batch) { return static_cast<size_t>(batch) * 12; };
+  return launch(reserve_kernel, dim3(1), kTableThreads, smem(p.batch), smem(kMaxPlanBatch), stream, p);
 }
 
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
-  const size_t smem = static_cast<size_t>(p.count) * 16 + static_cast<size_t>(p.batch) * 4;
-  const cudaError_t e = launch(fork_plan_kernel, dim3(1), kTableThreads, smem, stream, p);
+  const auto smem = [](int32_t count, int32_t batch) { return static_cast<size_t>(count) * 16 + static_cast<size_t>(batch) * 4; };
+  const cudaError_t e = launch(fork_plan_kernel, dim3(1), kTableThreads, smem(p.count, p.batch), smem(kMaxPlanBatch, kMaxPlanBatch),
+                               stream, p);
   if (e != cudaSuccess) return e;
-  return launch(fork_copy_kernel, dim3(p.count, 2 * p.hkv), kCopyThreads, 0, stream, p);
+  return launch(fork_copy_kernel, dim3(p.count, 2 * p.hkv), kCopyThreads, 0, 0, stream, p);
 }
 
 cudaError_t launch_free(const FreeParams& p, cudaStream_t stream) {
-  return launch(free_kernel, dim3(p.count), kFreeThreads, 0, stream, p);
+  return launch(free_kernel, dim3(p.count), kFreeThreads, 0, 0, stream, p);
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
-  const cudaError_t e = launch(compact_move_kernel, dim3(p.batch, 2 * p.hkv), kCompactThreads, 0, stream, p);
+  const cudaError_t e = launch(compact_move_kernel, dim3(p.batch, 2 * p.hkv), kCompactThreads, 0, 0, stream, p);
   if (e != cudaSuccess) return e;
-  return launch(compact_table_kernel, dim3(p.batch), kFreeThreads, 0, stream, p);
+  return launch(compact_table_kernel, dim3(p.batch), kFreeThreads, 0, 0, stream, p);
 }
 
 }  // namespace fd

@@ -669,26 +669,20 @@ __global__ void __launch_bounds__(kMaxPlanThreads, 1) plan_chunk_kernel(PlanPara
 }  // namespace
 
 cudaError_t launch_plan_chunk(const PlanParams& p, cudaStream_t stream) {
-  const size_t smem = sizeof(int32_t) * (14 * static_cast<size_t>(p.B) + 5);
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(plan_chunk_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  const auto smem_of = [](int32_t batch) { return sizeof(int32_t) * (14 * static_cast<size_t>(batch) + 5); };
+  const size_t smem = smem_of(p.B);
+  const cudaError_t e = allow_dynamic_smem(plan_chunk_kernel, smem, smem_of(kMaxPlanBatch));
+  if (e != cudaSuccess) return e;
   plan_chunk_kernel<<<kPlanChunkCtas, kMaxPlanThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_plan_decode(const PlanParams& p, cudaStream_t stream) {
-  const size_t smem = sizeof(int32_t) * (7 * static_cast<size_t>(p.B) + 2);
+  const auto smem_of = [](int32_t batch) { return sizeof(int32_t) * (7 * static_cast<size_t>(batch) + 2); };
+  const size_t smem = smem_of(p.B);
   const int threads = kMaxPlanThreads;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(plan_decode_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_dynamic_smem(plan_decode_kernel, smem, smem_of(kMaxPlanBatch));
+  if (e != cudaSuccess) return e;
   plan_decode_kernel<<<1, threads, smem, stream>>>(p);
   return cudaGetLastError();
 }
