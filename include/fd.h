@@ -409,7 +409,8 @@ size_t fd_tree_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_q_
  *  k_new, v_new [T, Hkv, D]  the pages' dtype (FD_F32 or FD_BF16); any strides that are multiples
  *               of 16 bytes, each tensor its own
  * and goes to position start_lens[b] + i of the sequence, whose pages must stand in its row and
- * belong to it alone there (fd_pages_reserve gives them). cache_lens is not involved.
+ * belong to it alone there (fd_pages_reserve gives them). cache_lens is not involved. Like the attention
+ * calls, it takes a position's entry as it stands, without a look at the entries before it.
  *  start_lens, new_lens [batch] int32 (device). A negative new_lens counts as 0, a negative start
  *               skips its sequence, positions beyond the row's capacity are not written
  *               (FD_FLAG_LEN_CLAMPED); a position whose entry is outside the pool is not written
@@ -433,7 +434,7 @@ fd_status fd_pages_append_fp8(const fd_tensor* k_new, const fd_tensor* v_new, fd
  * fd_pages_reserve — give every sequence the pages for want_lens[b] tokens.
  *
  * A sequence with fewer than ceil(want_lens[b] / page_size) pages gets the missing ones (references
- * 1). Sequences are served in order while the free pages last: the first one whose missing pages are
+ * 1), and the entry behind them becomes -1 where the row goes on. Sequences are served in order while the free pages last: the first one whose missing pages are
  * not all there, and every later one that misses any, get none (FD_FLAG_POOL_FULL). A want beyond
  * the row's capacity counts as the capacity (FD_FLAG_LEN_CLAMPED).
  */

@@ -411,6 +411,12 @@ __global__ void __launch_bounds__(kTableThreads) reserve_kernel(const ReservePar
     *entry(rank) = page;
     p.page_refs[page] = 1;
   });
+  // a sequence ends behind its new pages: what stood behind the first negative entry does not join it
+  for (int b = threadIdx.x; b < p.batch; b += kTableThreads) {
+    const int64_t missing = s_sum[b] - (b > 0 ? s_sum[b - 1] : 0), pages = s_have[b] + missing;
+    if (missing > 0 && s_sum[b] <= got && pages < p.pages_per_seq)
+      p.block_table[static_cast<int64_t>(b) * p.pages_per_seq + pages] = -1;
+  }
   if (got < need) {
     if (threadIdx.x == 0) atomicOr(p.status, FD_FLAG_POOL_FULL);
     __syncthreads();
