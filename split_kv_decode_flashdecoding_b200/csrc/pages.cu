@@ -156,8 +156,8 @@ __device__ __forceinline__ void append_load(AppendUnit<S, kFp8>& a, const S* src
 }
 
 // x / s rounded to fp32 as the division rounds it: one Newton step on x times the rounded reciprocal r
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), for s
-// with a normal reciprocal. A zero's sign may be lost. Not for quotients near overflow, whose step would
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990), for
+// scales whose reciprocal the host gives (not 0). A zero's sign may be lost. Not for quotients near overflow, whose step would
 // be NaN: those above 1e6 stay as the product gives them.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = x * r;
@@ -208,7 +208,7 @@ __device__ __forceinline__ uint4 append_convert(const AppendUnit<S, kFp8>& a, fl
         const uint64_t rest = fma_f32x2(q[i], s2, pair_f32(x[2 * i], x[2 * i + 1]));
         unpair_f32(fma_f32x2(rest, r2, q[i]), x[2 * i], x[2 * i + 1]);
       }
-    } else {  // a large value, or a scale without a normal reciprocal (recip 0)
+    } else {  // a large value, or a scale that is divided by (recip 0)
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = recip != 0.f ? quotient(x[i], scale, recip) : __fdiv_rn(x[i], scale);
     }

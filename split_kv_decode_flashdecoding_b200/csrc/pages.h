@@ -17,7 +17,7 @@ struct AppendParams {
   int64_t rows;
   int32_t batch, pages_per_seq, num_pages, page_size, hkv, d;
   float k_scale, v_scale;             // E4M3 pages
-  float k_recip, v_recip;             // their reciprocals, 0 where those are not normal numbers
+  float k_recip, v_recip;             // their reciprocals, 0: divide by the scale
   int32_t rows_per_cta;
   uint32_t* status;
 };

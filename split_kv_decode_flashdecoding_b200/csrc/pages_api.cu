@@ -121,9 +121,13 @@ fd_status append(const fd_tensor* k_new, const fd_tensor* v_new, fd_tensor* k, f
   p.d = static_cast<int32_t>(k->shape[3]);
   p.k_scale = k_scale;
   p.v_scale = v_scale;
+  // quotient()'s Newton step needs a normal reciprocal, and a rest x - q s that no rounding touches. q
+  // from 2^-11 on (smaller ones are code 0 whatever their last bits) has its last bit at 2^-34 or above, s
+  // from 2^e on at 2^(e - 23): their product is a multiple of 2^(e - 57), an fp32 number's last bit 2^-149
+  // or more from e = -92 on.
   const auto recip = [](float s) {
     const float r = 1.f / s;
-    return s >= FLT_MIN && r >= FLT_MIN && r <= FLT_MAX ? r : 0.f;
+    return s >= 0x1p-90f && r >= FLT_MIN ? r : 0.f;
   };
   p.k_recip = recip(k_scale);
   p.v_recip = recip(v_scale);
