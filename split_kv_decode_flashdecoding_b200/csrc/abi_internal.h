@@ -76,8 +76,9 @@ fd_status decode_call(const fd_tensor* q, const fd_tensor* k_cache, const fd_ten
                       const PresetScratch* preset = nullptr);
 
 // The status word of the allocation-free entry point's scratch on the current device, read and
-// cleared (0 when that scratch has not been set up on the device). The caller synchronises.
-fd_status static_scratch_take_status(uint32_t* flags);
+// cleared on `stream` (0 when that scratch has not been set up on the device). Waits for the read;
+// the caller orders what comes after the clear.
+fd_status static_scratch_take_status(cudaStream_t stream, uint32_t* flags);
 
 // Persistent CTAs of the split kernel on device `dev`.
 int decode_ctas(int dev, bool use_tc);

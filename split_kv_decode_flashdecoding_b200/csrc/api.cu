@@ -1010,20 +1010,25 @@ fd_status fd_poll_status(void* stream_, uint32_t* flags) {
       buffers.push_back(it->second.ptr);
     }
   }
+  // All on the polled stream: what is cleared is cleared before its next call runs, and the poll waits for
+  // no other stream's work (the legacy stream's copies would).
   uint32_t v = 0;
   for (void* ptr : buffers) {
     uint32_t one = 0;
-    FD_CUDA(cudaMemcpy(&one, ptr, sizeof(one), cudaMemcpyDeviceToHost), "read status");
-    const uint32_t zero = 0;
-    FD_CUDA(cudaMemcpy(ptr, &zero, sizeof(zero), cudaMemcpyHostToDevice), "clear status");
+    FD_CUDA(cudaMemcpyAsync(&one, ptr, sizeof(one), cudaMemcpyDeviceToHost, stream), "read status");
+    FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
+    if (one) FD_CUDA(cudaMemsetAsync(ptr, 0, sizeof(one), stream), "clear status");
     if (one & FD_FLAG_WAIT_TIMEOUT)  // a call that gave up may have left pieces counted
-      FD_CUDA(cudaMemset(static_cast<char*>(ptr) + offsetof(WsHeader, row_pieces), 0, sizeof(WsHeader::row_pieces)), "clear counters");
+      FD_CUDA(cudaMemsetAsync(static_cast<char*>(ptr) + offsetof(WsHeader, row_pieces), 0, sizeof(WsHeader::row_pieces), stream),
+              "clear counters");
     v |= one;
   }
   // the status bits of fd_decode_attention_static calls on this device
   uint32_t st = 0;
-  fd_status s = static_scratch_take_status(&st);
+  fd_status s = static_scratch_take_status(stream, &st);
   if (s != FD_OK) return s;
+  // graphs that use these buffers may be replayed on other streams
+  if (v | st) FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
   *flags = v | st;
   return FD_OK;
 }

@@ -104,7 +104,7 @@ fd_status static_scratch_address(int dev, void** out) {
 
 namespace fd_abi {
 
-fd_status static_scratch_take_status(uint32_t* flags) {
+fd_status static_scratch_take_status(cudaStream_t stream, uint32_t* flags) {
   *flags = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -117,11 +117,11 @@ fd_status static_scratch_take_status(uint32_t* flags) {
     ptr = it->second.ptr;
   }
   uint32_t v = 0;
-  e = cudaMemcpy(&v, ptr, sizeof(v), cudaMemcpyDeviceToHost);
+  e = cudaMemcpyAsync(&v, ptr, sizeof(v), cudaMemcpyDeviceToHost, stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return cuda_fail(e, "read static scratch status");
-  const uint32_t zero = 0;
-  e = cudaMemcpy(ptr, &zero, sizeof(zero), cudaMemcpyHostToDevice);
-  if (e != cudaSuccess) return cuda_fail(e, "clear static scratch status");
+  if (v && (e = cudaMemsetAsync(ptr, 0, sizeof(v), stream)) != cudaSuccess)
+    return cuda_fail(e, "clear static scratch status");
   *flags = v;
   return FD_OK;
 }
