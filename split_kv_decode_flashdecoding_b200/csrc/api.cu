@@ -53,7 +53,9 @@ fd_status cuda_fail(cudaError_t e, const char* what) {
 struct Workspace {
   void* ptr = nullptr;
   size_t bytes = 0;
-  std::vector<void*> outgrown;  // smaller buffers it replaced, freed by fd_shutdown
+  uint32_t status = 0;          // flags of a buffer that was given back, for the next one's header
+  bool captured = false;        // a captured call was given ptr: graphs may hold it
+  std::vector<void*> outgrown;  // smaller buffers that graphs may hold, freed by fd_shutdown
   cudaStream_t side = nullptr;
   cudaEvent_t fork = nullptr, join = nullptr;
 };
@@ -65,28 +67,45 @@ fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace*
   FD_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
   std::lock_guard<std::mutex> lock(g_mu);
   Workspace& w = g_ws[{dev, reinterpret_cast<uintptr_t>(stream)}];
+  // (the legacy stream has no status of its own while another stream is captured: it is not)
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
+    (void)cudaGetLastError();
+    cs = cudaStreamCaptureStatusNone;
+  }
   if (w.ptr && w.bytes >= need) {
+    w.captured |= cs != cudaStreamCaptureStatusNone;
     *out = w.ptr;
     if (view) *view = w;
     return FD_OK;
   }
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  FD_CUDA(cudaStreamIsCapturing(stream, &cs), "cudaStreamIsCapturing");
   if (cs != cudaStreamCaptureStatusNone)
     return fail(FD_ERR_WORKSPACE,
                 "workspace of this stream holds %zu bytes but the call needs %zu; reserve it with "
                 "fd_reserve_workspace before capturing",
                 w.bytes, need);
-  // A buffer that is outgrown stays allocated until fd_shutdown: graphs captured with it may still
-  // be replayed. A new one is twice as large where memory allows it, so that what is kept stays
-  // below the current one's size.
+  // A buffer that a captured call used stays allocated until fd_shutdown: its graph may still be
+  // replayed. The new one is then twice as large where memory allows it, so that what is kept stays
+  // below the current one's size. Any other buffer is given back first.
   const auto rounded = [](size_t n) { return (n + (2u << 20) - 1) / (2u << 20) * (2u << 20); };
-  size_t nb = rounded(std::max({need, static_cast<size_t>(1) << 20, 2 * w.bytes}));
+  const size_t least = rounded(std::max(need, static_cast<size_t>(1) << 20));
+  size_t nb = least;
+  if (w.ptr && w.captured) {
+    nb = std::max(nb, 2 * w.bytes);
+  } else if (w.ptr) {
+    uint32_t status = 0;
+    FD_CUDA(cudaMemcpyAsync(&status, w.ptr, sizeof(status), cudaMemcpyDeviceToHost, stream), "read status");
+    FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
+    w.status |= status;
+    FD_CUDA(cudaFree(w.ptr), "cudaFree(workspace)");
+    w.ptr = nullptr;
+    w.bytes = 0;
+  }
   void* p = nullptr;
   cudaError_t e = cudaMalloc(&p, nb);
-  if (e != cudaSuccess && rounded(need) < nb) {
+  if (e != cudaSuccess && least < nb) {
     (void)cudaGetLastError();
-    nb = rounded(need);
+    nb = least;
     e = cudaMalloc(&p, nb);
   }
   if (e != cudaSuccess) {
@@ -96,11 +115,14 @@ fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace*
   }
   WsHeader h;
   std::memset(&h, 0, sizeof(h));
+  h.status = w.status;
   FD_CUDA(cudaMemcpyAsync(p, &h, sizeof(h), cudaMemcpyHostToDevice, stream), "init workspace");
   FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
   if (w.ptr) w.outgrown.push_back(w.ptr);
   w.ptr = p;
   w.bytes = nb;
+  w.status = 0;
+  w.captured = false;
   if (!w.side) {
     int prio_lo = 0, prio_hi = 0;
     FD_CUDA(cudaDeviceGetStreamPriorityRange(&prio_lo, &prio_hi), "cudaDeviceGetStreamPriorityRange");
