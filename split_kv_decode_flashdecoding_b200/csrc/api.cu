@@ -51,8 +51,8 @@ fd_status cuda_fail(cudaError_t e, const char* what) {
 // first buffer, so a call under graph capture (which must find the buffer reserved) never
 // creates them.
 struct Workspace {
-  void* ptr = nullptr;
-  size_t bytes = 0;
+  void* ptr = nullptr;          // behind its WsFront
+  size_t bytes = 0;             // from ptr on
   uint32_t status = 0;          // flags of a buffer that was given back, for the next one's header
   bool captured = false;        // a captured call was given ptr: graphs may hold it
   std::vector<void*> outgrown;  // smaller buffers that graphs may hold, freed by fd_shutdown
@@ -61,6 +61,9 @@ struct Workspace {
 };
 std::mutex g_mu;
 std::map<std::pair<int, uintptr_t>, Workspace> g_ws;
+
+// What stands in front of a workspace, and where its allocation begins.
+WsFront* ws_front(void* ws) { return static_cast<WsFront*>(ws) - 1; }
 
 fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace* view) {
   int dev = 0;
@@ -87,37 +90,45 @@ fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace*
   // A buffer that a captured call used stays allocated until fd_shutdown: its graph may still be
   // replayed. The new one is then twice as large where memory allows it, so that what is kept stays
   // below the current one's size. Any other buffer is given back first.
-  const auto rounded = [](size_t n) { return (n + (2u << 20) - 1) / (2u << 20) * (2u << 20); };
+  // Allocations, with what stands in front, are whole units of 2 MB.
+  const auto rounded = [](size_t n) {
+    constexpr size_t unit = 2u << 20;
+    return (n + sizeof(WsFront) + unit - 1) / unit * unit - sizeof(WsFront);
+  };
   const size_t least = rounded(std::max(need, static_cast<size_t>(1) << 20));
   size_t nb = least;
   if (w.ptr && w.captured) {
-    nb = std::max(nb, 2 * w.bytes);
+    nb = std::max(nb, rounded(2 * w.bytes));
   } else if (w.ptr) {
     uint32_t status = 0;
     FD_CUDA(cudaMemcpyAsync(&status, w.ptr, sizeof(status), cudaMemcpyDeviceToHost, stream), "read status");
     FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
     w.status |= status;
-    FD_CUDA(cudaFree(w.ptr), "cudaFree(workspace)");
+    FD_CUDA(cudaFree(ws_front(w.ptr)), "cudaFree(workspace)");
     w.ptr = nullptr;
     w.bytes = 0;
   }
-  void* p = nullptr;
-  cudaError_t e = cudaMalloc(&p, nb);
+  void* front = nullptr;
+  cudaError_t e = cudaMalloc(&front, sizeof(WsFront) + nb);
   if (e != cudaSuccess && least < nb) {
     (void)cudaGetLastError();
     nb = least;
-    e = cudaMalloc(&p, nb);
+    e = cudaMalloc(&front, sizeof(WsFront) + nb);
   }
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return fail(FD_ERR_WORKSPACE, "cudaMalloc of %zu workspace bytes failed: %s", nb,
                 cudaGetErrorString(e));
   }
-  WsHeader h;
+  struct {
+    WsFront front;
+    WsHeader header;
+  } h;
   std::memset(&h, 0, sizeof(h));
-  h.status = w.status;
-  FD_CUDA(cudaMemcpyAsync(p, &h, sizeof(h), cudaMemcpyHostToDevice, stream), "init workspace");
+  h.header.status = w.status;
+  FD_CUDA(cudaMemcpyAsync(front, &h, sizeof(h), cudaMemcpyHostToDevice, stream), "init workspace");
   FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
+  void* p = static_cast<char*>(front) + sizeof(WsFront);
   if (w.ptr) w.outgrown.push_back(w.ptr);
   w.ptr = p;
   w.bytes = nb;
@@ -1041,8 +1052,7 @@ fd_status fd_poll_status(void* stream_, uint32_t* flags) {
     FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
     if (one) FD_CUDA(cudaMemsetAsync(ptr, 0, sizeof(one), stream), "clear status");
     if (one & FD_FLAG_WAIT_TIMEOUT)  // a call that gave up may have left pieces counted
-      FD_CUDA(cudaMemsetAsync(static_cast<char*>(ptr) + offsetof(WsHeader, row_pieces), 0, sizeof(WsHeader::row_pieces), stream),
-              "clear counters");
+      FD_CUDA(cudaMemsetAsync(ws_front(ptr), 0, sizeof(WsFront), stream), "clear counters");
     v |= one;
   }
   // the status bits of fd_decode_attention_static calls on this device
@@ -1095,8 +1105,8 @@ void fd_shutdown(void) {
       cudaGetDevice(&cur);
       cudaSetDevice(kv.first.first);
       cudaDeviceSynchronize();
-      if (kv.second.ptr) cudaFree(kv.second.ptr);
-      for (void* ptr : kv.second.outgrown) cudaFree(ptr);
+      if (kv.second.ptr) cudaFree(ws_front(kv.second.ptr));
+      for (void* ptr : kv.second.outgrown) cudaFree(ws_front(ptr));
       if (kv.second.side) cudaStreamDestroy(kv.second.side);
       if (kv.second.fork) cudaEventDestroy(kv.second.fork);
       if (kv.second.join) cudaEventDestroy(kv.second.join);

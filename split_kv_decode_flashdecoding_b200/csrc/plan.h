@@ -77,11 +77,16 @@ struct WsHeader {
                             // between calls)
   int32_t tile_ctas;        // chunked prefill: CTAs the tile kernel keeps (least chunk_tile_cost)
   int32_t pad[57];
-  // attention of packed rows: pieces of a cut item that are done, by the item's first cut, one byte a
-  // softmax warp (zero between calls: the last piece's warp takes its item's count back)
+};
+static_assert(sizeof(WsHeader) == 256, "WsHeader is 256 bytes");
+
+// In front of every stream's workspace, beside the bytes that a call asks for. Attention of packed rows:
+// pieces of a cut item that are done, by the item's first cut, one byte a softmax warp (zero between
+// calls: the last piece's warp takes its item's count back).
+struct WsFront {
   uint32_t row_pieces[192][2];
 };
-static_assert(sizeof(WsHeader) == 1792, "WsHeader is 1792 bytes");
+static_assert(sizeof(WsFront) % 256 == 0, "the workspace behind it is 256-byte aligned");
 
 FD_HD int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // ceil(a / b) for 0 <= a < 2^31 and 0 < b < 2^31 in 32-bit unsigned arithmetic (a + b - 1 < 2^32),

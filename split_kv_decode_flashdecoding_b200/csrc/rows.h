@@ -31,6 +31,7 @@ struct RowsParams {
   int32_t q_box_rows;              // tokens of one Q box (G heads each): min(128 / G, rows)
   int32_t kv_box_rows;             // keys of one K or V box: min(128; rows, S_cap or page_size)
   WsHeader* hdr;
+  WsFront* front;                  // in front of hdr
   float *part_o, *part_ml;         // pieces of cut items, behind the header (launch_rows)
 };
 

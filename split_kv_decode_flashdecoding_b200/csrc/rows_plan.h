@@ -19,7 +19,7 @@ namespace fd {
 
 constexpr int32_t kItemFixed = 256;  // an item's fixed cost (Q, first scores, output): two key tiles
 constexpr int32_t kMinPiece = 4;     // key tiles of the smallest piece of a cut item
-constexpr int32_t kMaxRowCtas = 192; // CTAs of one call (merge counters in the workspace header)
+constexpr int32_t kMaxRowCtas = 192; // CTAs of one call (merge counters in front of the workspace)
 
 FD_HD int32_t rows_tile_tokens(int32_t g) { return kQTile / g; }
 FD_HD int32_t rows_items(int32_t n, int32_t span) { return cdiv32(n, span); }

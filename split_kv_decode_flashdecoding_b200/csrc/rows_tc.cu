@@ -311,7 +311,7 @@ __device__ __forceinline__ void row_output(const RowsParams& p, Smem& S, const R
   }
   part_ml[part * 256] = make_float2(m, l);
   __syncwarp();
-  uint32_t* counter = &p.hdr->row_pieces[it.cut0][warp >> 2];
+  uint32_t* counter = &p.front->row_pieces[it.cut0][warp >> 2];
   uint32_t before = 0;
   if (lane == 0) before = (atomic_add_acq_rel(counter, 1u << (8 * quad)) >> (8 * quad)) & 0xffu;
   before = __shfl_sync(0xffffffffu, before, 0);
@@ -1184,6 +1184,7 @@ size_t rows_workspace_bytes(int d, int nctas) {
 cudaError_t launch_rows(RowsParams p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, int nctas,
                         cudaStream_t stream) {
   char* base = reinterpret_cast<char*>(p.hdr);
+  p.front = reinterpret_cast<WsFront*>(base) - 1;
   p.part_o = reinterpret_cast<float*>(base + sizeof(WsHeader));
   p.part_ml = p.part_o + static_cast<int64_t>(2 * nctas) * 2 * 128 * p.d;
   const int src = p.prefix_lens == nullptr ? kSrcPacked : p.block_table ? kSrcPaged : kSrcCache;
