@@ -18,6 +18,11 @@ Functions keep the C names:
 * ``fd_pages_reserve``, ``fd_pages_append``, ``fd_pages_append_fp8``, ``fd_pages_fork``,
   ``fd_pages_compact``, ``fd_pages_free`` on a paged cache's device state
 * status, workspace and profiling helpers.
+
+``stream`` is a torch stream, a raw handle or None (the current stream). The prompt, tree and page calls
+tell torch's allocator when they use their tensors on a torch stream other than the current one, and
+take new results from that stream's memory; with a raw handle, and with the other calls, the caller
+keeps the tensors until the stream is done with them.
 """
 
 from __future__ import annotations

@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/Functions.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -13,6 +14,7 @@
 
 #include <initializer_list>
 #include <limits>
+#include <optional>
 #include <utility>
 
 #include "fd.h"
@@ -72,26 +74,56 @@ float to_float(PyObject* o) {
   return static_cast<float>(x);
 }
 
-// None: the device's current stream; else a torch.cuda.Stream or a raw handle.
-void* stream_of(PyObject* o, c10::DeviceIndex index) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(index).stream();
-  PyObject* handle = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Long(o);
-  if (!handle) throw python_error();
-  void* s = PyLong_AsVoidPtr(handle);
-  Py_DECREF(handle);
-  if (!s && PyErr_Occurred()) throw python_error();
-  return s;
+int64_t attribute(PyObject* o, const char* name) {
+  PyObject* x = PyObject_GetAttrString(o, name);
+  if (!x) throw python_error();
+  const long long v = PyLong_AsLongLong(x);
+  Py_DECREF(x);
+  if (v == -1 && PyErr_Occurred()) throw python_error();
+  return v;
 }
 
-// call(stream) on the tensor's device, without the interpreter lock.
+// The stream of a call: the device's current one (None), a torch stream, or a raw handle (an integer, or
+// another library's object with one). `side` is a torch stream other than the current one: the
+// allocator, which takes the memory of a dropped tensor back for the stream that it came from, has to
+// know that the call's tensors are used there too. A raw handle says nothing about how long its stream
+// lives; its caller keeps the tensors until the work is done, as in C.
+struct Lane {
+  void* handle = nullptr;
+  std::optional<c10::cuda::CUDAStream> side;
+  Lane(PyObject* o, c10::Device dev) {
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(dev.index());
+    if (o == Py_None) {
+      handle = now.stream();
+    } else if (PyObject_HasAttrString(o, "stream_id")) {
+      const int64_t type = attribute(o, "device_type"), index = attribute(o, "device_index");
+      TORCH_CHECK_VALUE(type == static_cast<int64_t>(c10::DeviceType::CUDA) && index == dev.index(), "the stream is not one of ", dev);
+      const auto s = c10::cuda::CUDAStream::unpack3(attribute(o, "stream_id"), dev.index(), c10::DeviceType::CUDA);
+      handle = s.stream();
+      if (handle != now.stream()) side = s;
+    } else {
+      PyObject* x = PyObject_HasAttrString(o, "cuda_stream") ? PyObject_GetAttrString(o, "cuda_stream") : PyNumber_Index(o);
+      if (!x) throw python_error();
+      handle = PyLong_AsVoidPtr(x);
+      Py_DECREF(x);
+      if (!handle && PyErr_Occurred()) throw python_error();
+    }
+  }
+};
+
+void record(const at::Tensor& t, c10::cuda::CUDAStream s) { c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), s); }
+
+// call(stream) on the tensor's device, without the interpreter lock. args: the call's n arguments.
 template <typename Call>
-void run(const char* name, const at::Tensor& like, PyObject* stream, Call call) {
-  void* s = stream_of(stream, like.device().index());
+void run(const char* name, const at::Tensor& like, const Lane& lane, PyObject* const* args, Py_ssize_t n, Call call) {
+  if (lane.side)
+    for (Py_ssize_t i = 0; i < n; ++i)
+      if (THPVariable_Check(args[i])) record(THPVariable_Unpack(args[i]), *lane.side);
   fd_status st;
   {
     const c10::cuda::CUDAGuard guard(like.device());
     Py_BEGIN_ALLOW_THREADS
-    st = call(s);
+    st = call(lane.handle);
     Py_END_ALLOW_THREADS
   }
   if (st == FD_OK) return;
@@ -103,20 +135,29 @@ void run(const char* name, const at::Tensor& like, PyObject* stream, Call call) 
 
 void count(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n); }
 
-// out [T, Hq, D] and lse [T, Hq] of an attention call: the caller's, or new ones.
+// out [T, Hq, D] and lse [T, Hq] of an attention call: the caller's, or new ones. New ones are the
+// stream's: memory that the current stream has still to write would be free to it otherwise.
 struct RowsOut {
   at::Tensor out, lse;
-  RowsOut(const at::Tensor& q, PyObject* o, PyObject* l) {
-    TORCH_CHECK_VALUE(q.dim() == 3, "q must be [T, Hq, D]");
-    out = o == Py_None ? at::empty(q.sizes(), q.options()) : tensor(o, "out");
+  RowsOut(const at::Tensor& q, PyObject* o, PyObject* l, const Lane& lane) {
     const at::IntArrayRef rows = q.sizes().slice(0, 2);
-    if (l == Py_None) {
-      lse = at::empty(rows, q.options().dtype(at::kFloat));
+    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(q.device().index());
+    const c10::cuda::CUDAStreamGuard guard(lane.side ? *lane.side : now);
+    if (o != Py_None) {
+      out = tensor(o, "out");
     } else {
+      out = at::empty(q.sizes(), q.options());
+      if (lane.side) record(out, now);
+    }
+    if (l != Py_None) {
       lse = tensor(l, "lse");
       TORCH_CHECK_VALUE(lse.scalar_type() == at::kFloat && lse.is_contiguous() && lse.sizes() == rows,
                         "lse must be a contiguous float32 tensor [T, Hq]");
+    } else {
+      lse = at::empty(rows, q.options().dtype(at::kFloat));
+      if (lane.side) record(lse, now);
     }
+    need(q, {{"out", &out}, {"lse", &lse}});
   }
   PyObject* give() const {
     PyObject* a = THPVariable_Wrap(out);
@@ -154,12 +195,14 @@ PyObject* prompt_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
   const int64_t batch = numel(a[3], "seq_lens");
   const int32_t* lens = int32s(a[3], "seq_lens", q.device(), {batch});
-  const RowsOut o(q, a[4], a[5]);
-  need(q, {{"k", &k}, {"v", &v}, {"out", &o.out}, {"lse", &o.lse}});
+  TORCH_CHECK_VALUE(q.dim() == 3, "q must be [T, Hq, D]");
+  need(q, {{"k", &k}, {"v", &v}});
+  const Lane lane(a[6], q.device());
+  const RowsOut o(q, a[4], a[5], lane);
   const fd_tensor dq = desc(q), dk = desc(k), dv = desc(v);
   fd_tensor d = desc(o.out);
   float* lse = static_cast<float*>(o.lse.data_ptr());
-  run("fd_prompt_attention", q, a[6],
+  run("fd_prompt_attention", q, lane, a, n,
       [&](void* s) { return fd_prompt_attention(&dq, &dk, &dv, lens, static_cast<int32_t>(batch), &d, lse, s); });
   return o.give();
   END_HANDLE_TH_ERRORS
@@ -185,13 +228,14 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t *prefix = int32s(a[4], "prefix_lens", dev, {batch}), *lens = int32s(a[5], "tree_lens", dev, {batch});
   const int64_t words = last(m);
   const int32_t* mask = int32s(a[6], "tree_mask", dev, {q.size(0), words});
-  const RowsOut o(q, a[7], a[8]);
-  need(q, {{paged ? "k_pages" : "k_cache", &k}, {paged ? "v_pages" : "v_cache", &v}, {"out", &o.out}, {"lse", &o.lse}});
+  need(q, {{paged ? "k_pages" : "k_cache", &k}, {paged ? "v_pages" : "v_cache", &v}});
+  const Lane lane(a[9], dev);
+  const RowsOut o(q, a[7], a[8], lane);
   const fd_tensor dq = desc(q), dk = desc(k), dv = desc(v);
   fd_tensor d = desc(o.out);
   float* lse = static_cast<float*>(o.lse.data_ptr());
   const int32_t w = static_cast<int32_t>(words), b = static_cast<int32_t>(batch);
-  run(paged ? "fd_tree_attention_paged" : "fd_tree_attention", q, a[9], [&](void* s) {
+  run(paged ? "fd_tree_attention_paged" : "fd_tree_attention", q, lane, a, n, [&](void* s) {
     return paged ? fd_tree_attention_paged(&dq, &dk, &dv, table, per, b, prefix, lens, mask, w, &d, lse, s)
                  : fd_tree_attention(&dq, &dk, &dv, prefix, lens, mask, w, &d, lse, s);
   });
@@ -212,7 +256,7 @@ PyObject* pages_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   need(kp, {{"k_new", &k}, {"v_new", &v}, {"v_pages", &vp}});
   const fd_tensor dk = desc(k), dv = desc(v);
   fd_tensor pk = desc(kp), pv = desc(vp);
-  run(fp8 ? "fd_pages_append_fp8" : "fd_pages_append", kp, a[9], [&](void* s) {
+  run(fp8 ? "fd_pages_append_fp8" : "fd_pages_append", kp, Lane(a[9], kp.device()), a, n, [&](void* s) {
     return fp8 ? fd_pages_append_fp8(&dk, &dv, &pk, &pv, ks, vs, t.data, t.per, t.batch, start, lens, s)
                : fd_pages_append(&dk, &dv, &pk, &pv, t.data, t.per, t.batch, start, lens, s);
   });
@@ -230,7 +274,7 @@ PyObject* pages_reserve(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Table t(a[1], dev);
   const int32_t *want = int32s(a[2], "want_lens", dev, {t.batch}), size = to_int32(a[3], "page_size");
   need(r, {});
-  run("fd_pages_reserve", r, a[4], [&](void* s) {
+  run("fd_pages_reserve", r, Lane(a[4], dev), a, n, [&](void* s) {
     return fd_pages_reserve(refs, static_cast<int32_t>(r.numel()), t.data, t.per, t.batch, want, size, s);
   });
   Py_RETURN_NONE;
@@ -251,7 +295,7 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t *src = int32s(a[5], "src_seqs", dev, {pairs}), *dst = int32s(a[6], "dst_seqs", dev, {pairs});
   need(k, {{"v_pages", &v}});
   fd_tensor dk = desc(k), dv = desc(v);
-  run("fd_pages_fork", k, a[7], [&](void* s) {
+  run("fd_pages_fork", k, Lane(a[7], dev), a, n, [&](void* s) {
     return fd_pages_fork(&dk, &dv, refs, t.data, t.per, t.batch, lens, src, dst, static_cast<int32_t>(pairs), s);
   });
   Py_RETURN_NONE;
@@ -270,7 +314,7 @@ PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t listed = numel(a[3], "seqs");
   const int32_t* seqs = int32s(a[3], "seqs", dev, {listed});
   need(r, {});
-  run("fd_pages_free", r, a[4], [&](void* s) {
+  run("fd_pages_free", r, Lane(a[4], dev), a, n, [&](void* s) {
     return fd_pages_free(refs, static_cast<int32_t>(r.numel()), t.data, t.per, t.batch, lens, seqs, static_cast<int32_t>(listed), s);
   });
   Py_RETURN_NONE;
@@ -292,7 +336,7 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t* keep = int32s(a[6], "keep", dev, {t.batch, most});
   need(k, {{"v_pages", &v}});
   fd_tensor dk = desc(k), dv = desc(v);
-  run("fd_pages_compact", k, a[8], [&](void* s) {
+  run("fd_pages_compact", k, Lane(a[8], dev), a, n, [&](void* s) {
     return fd_pages_compact(&dk, &dv, refs, t.data, t.per, t.batch, lens, start, keep, static_cast<int32_t>(most), kept, s);
   });
   Py_RETURN_NONE;
