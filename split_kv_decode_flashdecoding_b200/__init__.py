@@ -147,12 +147,31 @@ def _check(status: int, what: str) -> None:
                               f"{lib.fd_last_error_message().decode()}")
 
 
-# the compiled marshalling of the serving calls (csrc/binding.cpp), linked to this libfd.so
-if not os.path.exists(os.path.join(os.path.dirname(LIB_PATH), "_fd_binding.so")):
-    raise ImportError("_fd_binding.so is missing beside libfd.so: build it with "
-                      "`python split_kv_decode_flashdecoding_b200/build.py`")
-_fd_binding = importlib.import_module("._fd_binding", __name__)
-_fd_binding.set_raise(_check)
+class _NoBinding:
+    """Stands in for the compiled module where it cannot be loaded: the calls that need it say why."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"fd_{name} needs _fd_binding.so, built beside libfd.so by `python "
+                          f"split_kv_decode_flashdecoding_b200/build.py` for the torch that runs it: {self._why}")
+
+
+def _load_binding():
+    try:
+        module = importlib.import_module("._fd_binding", __name__)
+    except ImportError as e:
+        return _NoBinding(e)
+    if module.torch_version != torch.__version__:
+        return _NoBinding(f"it was built for torch {module.torch_version}, this is {torch.__version__}")
+    module.set_raise(_check)
+    return module
+
+
+# the compiled marshalling of the serving calls (csrc/binding.cpp), linked to this libfd.so; the other
+# calls do without it
+_fd_binding = _load_binding()
 
 
 # an E4M3 cache may be passed as torch.float8_e4m3fn or as its uint8 codes

@@ -15,6 +15,7 @@ import argparse
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -26,6 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfd.so")
 BINDING = os.path.join(PKG, "_fd_binding.so")
+BINDING_STAMP = os.path.join(BUILD, "_fd_binding.txt")  # what BINDING was built for
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
@@ -80,14 +82,32 @@ def _torch_dir() -> str:
     return list(spec.submodule_search_locations)[0]
 
 
+def _torch_version() -> str:
+    with open(os.path.join(_torch_dir(), "version.py"), encoding="utf-8") as f:
+        return re.search(r"^__version__ = ['\"](.+)['\"]", f.read(), re.M).group(1)
+
+
+def _binding_is_for() -> str:
+    """What the module depends on besides its source: torch's and Python's binary interfaces."""
+    return f"torch {_torch_version()} in {_torch_dir()}, python {sysconfig.get_config_var('SOABI')}"
+
+
+def binding_up_to_date() -> bool:
+    if not _newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "fd.h")]) or not os.path.exists(BINDING_STAMP):
+        return False
+    with open(BINDING_STAMP, encoding="utf-8") as f:
+        return f.read() == _binding_is_for()
+
+
 def build_binding(force: bool = False) -> str:
     """Compile csrc/binding.cpp against torch and libfd.so (which has to be there); returns its path."""
-    if not force and _newer(BINDING, [BINDING_SRC, os.path.join(INCLUDE, "fd.h")]):
+    if not force and binding_up_to_date():
         return BINDING
     torch_dir, cuda = _torch_dir(), os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cxx = shutil.which("g++") or "c++"
     tmp = BINDING + ".tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f'-DFD_TORCH_VERSION="{_torch_version()}"',
            *(x for d in (os.path.join(torch_dir, "include"), sysconfig.get_paths()["include"], os.path.join(cuda, "include"))
              for x in ("-isystem", d)),
            "-I", INCLUDE, BINDING_SRC, "-o", tmp, "-L", PKG, "-l:libfd.so", "-L", os.path.join(torch_dir, "lib"),
@@ -97,6 +117,9 @@ def build_binding(force: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"building the binding failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(BINDING_STAMP, "w", encoding="utf-8") as f:
+        f.write(_binding_is_for())
     return BINDING
 
 

@@ -358,4 +358,8 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fd_binding", nullptr, -1, kMetho
 
 }  // namespace
 
-extern "C" PyMODINIT_FUNC PyInit__fd_binding() { return PyModule_Create(&kModule); }
+extern "C" PyMODINIT_FUNC PyInit__fd_binding() {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "torch_version", FD_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}
