@@ -15,8 +15,7 @@ namespace fd {
 struct RowsParams {
   const void *q, *k, *v;
   int64_t q_sr, q_sh;              // element strides of row and head
-  int64_t k_sr, k_sh, v_sr, v_sh;  // prompt: of k and v
-  int64_t kv_sb, kv_sh;            // tree: strides of sequence (page) and head
+  int64_t k_sr, k_sh, v_sr, v_sh;  // prompt: of k and v (a cache's are in the tensor maps)
   void* out;
   int64_t o_sr, o_sh;
   float* lse;                      // [rows][Hq]

@@ -136,8 +136,6 @@ fd_status tree(const fd_tensor* q, const fd_tensor* k, const fd_tensor* v, const
   if (!lse) return fail(FD_ERR_INVALID_ARGUMENT, "lse is NULL");
   p.k = k->data;
   p.v = v->data;
-  p.kv_sb = k->stride[0];
-  p.kv_sh = k->stride[1];
   p.lse = lse;
   p.row_lens = tree_lens;
   p.prefix_lens = prefix_lens;

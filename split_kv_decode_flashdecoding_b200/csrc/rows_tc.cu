@@ -64,7 +64,7 @@ struct RowItem {
   // The i-th tile of lane L is tile0 + i, or tile0 + 2 i + L (alt).
   int32_t tokens[2], used[2], kend[2];
   int32_t whole;              // this CTA has all its key tiles; if not, when cfull has arrived:
-  int32_t cut0, cuts, piece;  // rows_cuts of the item, this piece's index
+  int32_t cut0, cuts;         // rows_cuts of the item
 };
 
 // kPairs: items of two row tiles. Of one tile, its Q serves both lanes, and V has a stage more for it: a V
@@ -692,7 +692,6 @@ __global__ void __launch_bounds__(kRwThreads, 1)
               RowItem& it = S.item[slot];
               it.cut0 = cut0;
               it.cuts = cuts;
-              it.piece = cta + 1 - cut0;
             }
           }
           __syncwarp();
