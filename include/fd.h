@@ -31,8 +31,10 @@
  *  - The library owns one grow-only device workspace per (device, stream) for its split plan and
  *    partial results, freed by fd_shutdown(). A call whose workspace must grow synchronises that
  *    stream once before reallocating; a buffer that a captured call used stays allocated until
- *    fd_shutdown(), so that its graph may still be replayed. Calls captured on one stream share that stream's workspace: their
- *    graphs must not run at the same time (capture them on streams of their own for that).
+ *    fd_shutdown(), so that its graph may still be replayed. Calls captured on one stream share
+ *    that stream's workspace: their graphs must not run at the same time (capture them on streams
+ *    of their own for that). Host threads may call on one stream at the same time: each call
+ *    enqueues its kernels as a whole.
  *  - Errors: argument errors return before any launch (FD_ERR_INVALID_ARGUMENT /
  *    FD_ERR_UNSUPPORTED). CUDA errors map to FD_ERR_CUDA. fd_last_error_message() gives the
  *    detail for the calling thread. Nothing aborts or throws across the ABI.

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "../../include/fd.h"
 
 namespace fd_abi {
@@ -16,9 +18,16 @@ fd_status fail(fd_status s, const char* fmt, ...);
 fd_status cuda_fail(cudaError_t e, const char* what);
 
 // Device workspace of (current device, `stream`): at least `need` bytes, grown when the stream is
-// not being captured. `view` (may be nullptr) also gets the stream's side stream and events.
+// not being captured. It is the caller's as long as `use` lives, that is, until all kernels of the call are
+// enqueued: other threads' calls on the stream wait, so that they neither put their kernels between
+// this call's nor give its buffer back. `view` (may be nullptr) also gets the stream's side stream and
+// events.
 struct Workspace;
-fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace* view);
+class WorkspaceUse {
+  std::unique_lock<std::mutex> lock;
+  friend fd_status get_workspace(cudaStream_t stream, size_t need, WorkspaceUse* use, void** out, Workspace* view);
+};
+fd_status get_workspace(cudaStream_t stream, size_t need, WorkspaceUse* use, void** out, Workspace* view);
 
 int sm_count(int dev);
 

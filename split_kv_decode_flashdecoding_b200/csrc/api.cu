@@ -59,17 +59,26 @@ struct Workspace {
   cudaStream_t side = nullptr;
   cudaEvent_t fork = nullptr, join = nullptr;
 };
-std::mutex g_mu;
-std::map<std::pair<int, uintptr_t>, Workspace> g_ws;
+struct Slot {
+  std::mutex mu;  // held by a call while it enqueues its kernels
+  Workspace w;
+};
+std::mutex g_mu;  // of the map; a slot stays where it is until fd_shutdown
+std::map<std::pair<int, uintptr_t>, Slot> g_ws;
 
 // What stands in front of a workspace, and where its allocation begins.
 WsFront* ws_front(void* ws) { return static_cast<WsFront*>(ws) - 1; }
 
-fd_status get_workspace(cudaStream_t stream, size_t need, void** out, Workspace* view) {
+fd_status get_workspace(cudaStream_t stream, size_t need, WorkspaceUse* use, void** out, Workspace* view) {
   int dev = 0;
   FD_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
-  std::lock_guard<std::mutex> lock(g_mu);
-  Workspace& w = g_ws[{dev, reinterpret_cast<uintptr_t>(stream)}];
+  Slot* slot;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    slot = &g_ws[{dev, reinterpret_cast<uintptr_t>(stream)}];
+  }
+  use->lock = std::unique_lock<std::mutex>(slot->mu);
+  Workspace& w = slot->w;
   // (the legacy stream has no status of its own while another stream is captured: it is not)
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
@@ -532,7 +541,8 @@ fd_status fd_split_plan_device(const int32_t* cache_lens, int32_t batch, int32_t
   const int64_t items = decode_max_items(batch, num_kv_heads, cache_capacity, num_splits, num_ctas);
   const WsLayout L = ws_layout(items, 0, batch, 0, 1, 1, num_kv_heads);
   void* ws = nullptr;
-  fd_status s = get_workspace(stream, L.total, &ws, nullptr);
+  WorkspaceUse use;
+  fd_status s = get_workspace(stream, L.total, &use, &ws, nullptr);
   if (s != FD_OK) return s;
   char* base = static_cast<char*>(ws);
   PlanParams pp{};
@@ -585,6 +595,7 @@ fd_status decode_call(const fd_tensor* q, const fd_tensor* k_cache, const fd_ten
   const int64_t max_slots = max_items;  // one partial slot (G heads) per split item
   const WsLayout L = ws_layout(max_items, 0, sh.B, max_slots, sh.hq, sh.d, sh.hkv);
   void* ws = nullptr;
+  WorkspaceUse use;
   if (preset) {
     if (L.total > preset->bytes)
       return fail(FD_ERR_UNSUPPORTED,
@@ -592,7 +603,7 @@ fd_status decode_call(const fd_tensor* q, const fd_tensor* k_cache, const fd_ten
                   "the %s; use fd_decode_attention",
                   L.total, preset->bytes, preset->name);
     ws = preset->base;
-  } else if ((s = get_workspace(stream, L.total, &ws, nullptr)) != FD_OK) {
+  } else if ((s = get_workspace(stream, L.total, &use, &ws, nullptr)) != FD_OK) {
     return s;
   }
   char* base = static_cast<char*>(ws);
@@ -850,7 +861,8 @@ fd_status fd_chunk_prefill_attention(const fd_tensor* q_chunk, const fd_tensor* 
   const WsLayout L = ws_layout(max_dec, max_tiles, static_cast<int64_t>(T) + 1, max_slots, hq, d, hkv);
   void* ws = nullptr;
   Workspace wv;
-  if ((s = get_workspace(stream, L.total, &ws, &wv)) != FD_OK) return s;
+  WorkspaceUse use;
+  if ((s = get_workspace(stream, L.total, &use, &ws, &wv)) != FD_OK) return s;
   char* base = static_cast<char*>(ws);
   WsHeader* hdr = reinterpret_cast<WsHeader*>(base);
   DecodeItem* items = reinterpret_cast<DecodeItem*>(base + L.dec_items);
@@ -1024,7 +1036,8 @@ size_t fd_chunk_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_q
 
 fd_status fd_reserve_workspace(size_t bytes, void* stream_) {
   void* ws = nullptr;
-  return get_workspace(static_cast<cudaStream_t>(stream_), std::max(bytes, sizeof(WsHeader)), &ws, nullptr);
+  WorkspaceUse use;
+  return get_workspace(static_cast<cudaStream_t>(stream_), std::max(bytes, sizeof(WsHeader)), &use, &ws, nullptr);
 }
 
 fd_status fd_poll_status(void* stream_, uint32_t* flags) {
@@ -1033,16 +1046,20 @@ fd_status fd_poll_status(void* stream_, uint32_t* flags) {
   *flags = 0;
   int dev = 0;
   FD_CUDA(cudaGetDevice(&dev), "cudaGetDevice");
-  FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
-  std::vector<void*> buffers;  // the stream's workspace and those it has outgrown
+  Slot* slot = nullptr;
   {
     std::lock_guard<std::mutex> lock(g_mu);
     auto it = g_ws.find({dev, reinterpret_cast<uintptr_t>(stream)});
-    if (it != g_ws.end() && it->second.ptr) {
-      buffers = it->second.outgrown;
-      buffers.push_back(it->second.ptr);
-    }
+    if (it != g_ws.end()) slot = &it->second;
   }
+  std::unique_lock<std::mutex> use;
+  std::vector<void*> buffers;  // the stream's workspace and those it has outgrown
+  if (slot) {
+    use = std::unique_lock<std::mutex>(slot->mu);
+    buffers = slot->w.outgrown;
+    if (slot->w.ptr) buffers.push_back(slot->w.ptr);
+  }
+  FD_CUDA(cudaStreamSynchronize(stream), "cudaStreamSynchronize");
   // All on the polled stream: what is cleared is cleared before its next call runs, and the poll waits for
   // no other stream's work (the legacy stream's copies would).
   uint32_t v = 0;
@@ -1101,15 +1118,16 @@ void fd_shutdown(void) {
   {
     std::lock_guard<std::mutex> lock(g_mu);
     for (auto& kv : g_ws) {
+      Workspace& w = kv.second.w;
       int cur = 0;
       cudaGetDevice(&cur);
       cudaSetDevice(kv.first.first);
       cudaDeviceSynchronize();
-      if (kv.second.ptr) cudaFree(ws_front(kv.second.ptr));
-      for (void* ptr : kv.second.outgrown) cudaFree(ws_front(ptr));
-      if (kv.second.side) cudaStreamDestroy(kv.second.side);
-      if (kv.second.fork) cudaEventDestroy(kv.second.fork);
-      if (kv.second.join) cudaEventDestroy(kv.second.join);
+      if (w.ptr) cudaFree(ws_front(w.ptr));
+      for (void* ptr : w.outgrown) cudaFree(ws_front(ptr));
+      if (w.side) cudaStreamDestroy(w.side);
+      if (w.fork) cudaEventDestroy(w.fork);
+      if (w.join) cudaEventDestroy(w.join);
       cudaSetDevice(cur);
     }
     g_ws.clear();

@@ -64,14 +64,14 @@ fd_status check_new(const fd_tensor* t, const char* name, const fd_tensor* pages
 }
 
 // The workspace of the stream (status word, then `bytes` of scratch) and the device's SM count.
-fd_status scratch(cudaStream_t stream, size_t bytes, char** ws, int* nsm) {
+fd_status scratch(cudaStream_t stream, size_t bytes, WorkspaceUse* use, char** ws, int* nsm) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   *nsm = sm_count(dev);
   if (*nsm < 1) return fail(FD_ERR_CUDA, "no multiprocessors reported for device %d", dev);
   void* p = nullptr;
-  fd_status s = get_workspace(stream, sizeof(WsHeader) + bytes, &p, nullptr);
+  fd_status s = get_workspace(stream, sizeof(WsHeader) + bytes, use, &p, nullptr);
   *ws = static_cast<char*>(p);
   return s;
 }
@@ -95,9 +95,10 @@ fd_status append(const fd_tensor* k_new, const fd_tensor* v_new, fd_tensor* k, f
   if (batch == 0 || k_new->shape[0] == 0) return FD_OK;
   if (!block_table || !start_lens || !new_lens)
     return fail(FD_ERR_INVALID_ARGUMENT, "block_table / start_lens / new_lens is NULL");
+  WorkspaceUse use;
   char* ws = nullptr;
   int nsm = 0;
-  if ((s = scratch(stream, 0, &ws, &nsm)) != FD_OK) return s;
+  if ((s = scratch(stream, 0, &use, &ws, &nsm)) != FD_OK) return s;
   AppendParams p{};
   p.k_new = k_new->data;
   p.v_new = v_new->data;
@@ -166,9 +167,10 @@ fd_status fd_pages_reserve(int32_t* page_refs, int32_t num_pages, int32_t* block
   if (batch == 0) return FD_OK;
   if (!page_refs || !block_table || !want_lens)
     return fail(FD_ERR_INVALID_ARGUMENT, "page_refs / block_table / want_lens is NULL");
+  WorkspaceUse use;
   char* ws = nullptr;
   int nsm = 0;
-  if ((s = scratch(stream, 0, &ws, &nsm)) != FD_OK) return s;
+  if ((s = scratch(stream, 0, &use, &ws, &nsm)) != FD_OK) return s;
   ReserveParams p{};
   p.page_refs = page_refs;
   p.block_table = block_table;
@@ -194,9 +196,10 @@ fd_status fd_pages_fork(fd_tensor* k_pages, fd_tensor* v_pages, int32_t* page_re
   if (batch == 0) return fail(FD_ERR_INVALID_ARGUMENT, "%d pairs but no sequence", count);
   if (!page_refs || !block_table || !cache_lens || !src_seqs || !dst_seqs)
     return fail(FD_ERR_INVALID_ARGUMENT, "page_refs / block_table / cache_lens / src_seqs / dst_seqs is NULL");
+  WorkspaceUse use;
   char* ws = nullptr;
   int nsm = 0;
-  if ((s = scratch(stream, sizeof(int4) * static_cast<size_t>(count), &ws, &nsm)) != FD_OK) return s;
+  if ((s = scratch(stream, sizeof(int4) * static_cast<size_t>(count), &use, &ws, &nsm)) != FD_OK) return s;
   const int64_t es = static_cast<int64_t>(elem_size(k_pages->dtype));
   ForkParams p{};
   p.k_pages = k_pages->data;
@@ -231,9 +234,10 @@ fd_status fd_pages_free(int32_t* page_refs, int32_t num_pages, int32_t* block_ta
   if (count == 0) return FD_OK;
   if (!page_refs || !block_table || !cache_lens || !seqs)
     return fail(FD_ERR_INVALID_ARGUMENT, "page_refs / block_table / cache_lens / seqs is NULL");
+  WorkspaceUse use;
   char* ws = nullptr;
   int nsm = 0;
-  if ((s = scratch(stream, 0, &ws, &nsm)) != FD_OK) return s;
+  if ((s = scratch(stream, 0, &use, &ws, &nsm)) != FD_OK) return s;
   FreeParams p{};
   p.page_refs = page_refs;
   p.block_table = block_table;
@@ -259,9 +263,10 @@ fd_status fd_pages_compact(fd_tensor* k_pages, fd_tensor* v_pages, int32_t* page
   if (batch == 0) return FD_OK;
   if (!page_refs || !block_table || !cache_lens || !start_lens || !keep_lens || (max_keep > 0 && !keep))
     return fail(FD_ERR_INVALID_ARGUMENT, "page_refs / block_table / cache_lens / start_lens / keep / keep_lens is NULL");
+  WorkspaceUse use;
   char* ws = nullptr;
   int nsm = 0;
-  if ((s = scratch(stream, 4 * static_cast<size_t>(batch), &ws, &nsm)) != FD_OK) return s;
+  if ((s = scratch(stream, 4 * static_cast<size_t>(batch), &use, &ws, &nsm)) != FD_OK) return s;
   const int64_t es = static_cast<int64_t>(elem_size(k_pages->dtype));
   CompactParams p{};
   p.k_pages = k_pages->data;

@@ -71,7 +71,8 @@ fd_status run_rows(RowsParams* p, int kv_rank, const uint64_t* kd, const uint64_
   const int nctas = row_ctas(sm_count(dev));
   if (nctas < 1) return fail(FD_ERR_CUDA, "no multiprocessors reported for device %d", dev);
   void* ws = nullptr;
-  fd_status s = get_workspace(stream, rows_workspace_bytes(p->d, nctas), &ws, nullptr);
+  WorkspaceUse use;
+  fd_status s = get_workspace(stream, rows_workspace_bytes(p->d, nctas), &use, &ws, nullptr);
   if (s != FD_OK) return s;
   p->hdr = static_cast<WsHeader*>(ws);
   CUtensorMap tq, tk, tv;
