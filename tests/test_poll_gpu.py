@@ -23,6 +23,7 @@ def test_poll_does_not_wait_for_the_default_stream(static):
     if static:  # the static scratch holds a status word of its own
         fd.fd_decode_attention_static(q, kv, kv, lens, 0, out, lse)
     torch.cuda.synchronize()
+    fd.fd_poll_status(stream=s)  # what a test before left on this stream
     fd.fd_pages_reserve(refs, table, want, 8, stream=s)
     assert fd.fd_poll_status(stream=s) == 0
     torch.cuda._sleep(1_000_000_000)  # half a second of the default stream
@@ -41,6 +42,7 @@ def test_flags_of_calls_in_a_row():
     refs, table = _i32([0] * 4), _i32([[-1, -1]])
     good, bad = _i32([9]), _i32([100])
     torch.cuda.synchronize()
+    fd.fd_poll_status(stream=s)
     for _ in range(200):
         fd.fd_pages_reserve(refs, table, bad, 8, stream=s)
         assert fd.fd_poll_status(stream=s) == fd.FD_FLAG_LEN_CLAMPED

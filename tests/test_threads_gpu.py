@@ -73,6 +73,7 @@ def test_calls_of_several_threads_on_one_stream(grow):
     kinds = [Decode(), Rows(), Pages()]
     alone = torch.cuda.Stream()
     torch.cuda.synchronize()
+    fd.fd_poll_status(stream=alone)  # what a test before left on this stream
     want = [k.call(alone) for k in kinds]
     torch.cuda.synchronize()
     flags = fd.fd_poll_status(stream=alone)

@@ -8,6 +8,13 @@ pytestmark = pytest.mark.gpu
 MB = 1 << 20
 
 
+@pytest.fixture(autouse=True)
+def no_workspaces():
+    """torch hands its streams out again: one may hold a workspace of a test before."""
+    import split_kv_decode_flashdecoding_b200 as fd
+    fd.fd_shutdown()
+
+
 def _used():
     torch.cuda.synchronize()
     free, total = torch.cuda.mem_get_info()
