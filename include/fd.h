@@ -32,8 +32,8 @@
  *    partial results, freed by fd_shutdown(). A call whose workspace must grow synchronises that
  *    stream once before reallocating; a buffer that a captured call used stays allocated until
  *    fd_shutdown(), so that its graph may still be replayed. Calls captured on one stream share
- *    that stream's workspace: their graphs must not run at the same time (capture them on streams
- *    of their own for that). Host threads may call on one stream at the same time: each call
+ *    that stream's workspace: their graphs must not run at the same time, nor beside the stream's
+ *    own calls (capture them on streams of their own for that). Host threads may call on one stream at the same time: each call
  *    enqueues its kernels as a whole.
  *  - Errors: argument errors return before any launch (FD_ERR_INVALID_ARGUMENT /
  *    FD_ERR_UNSUPPORTED). CUDA errors map to FD_ERR_CUDA. fd_last_error_message() gives the
@@ -330,6 +330,9 @@ fd_status fd_decode_attention_static(const fd_tensor* q, const fd_tensor* k_cach
  *            log).
  * v must be finite in the rows of a request (a non-finite value may reach the request's other
  * rows); other rows may hold anything. out must not overlap q, k or v.
+ * The weights are rounded to one bf16 term for the product with v (the decode and chunk calls keep
+ * two): beside its own rounding, out is off by up to 2^-8 of sum_j p_j |v_j| / sum_j p_j. Sums and lse
+ * are fp32.
  */
 fd_status fd_prompt_attention(const fd_tensor* q, const fd_tensor* k, const fd_tensor* v,
                               const int32_t* seq_lens, int32_t batch, fd_tensor* out, float* lse,
@@ -362,6 +365,7 @@ size_t fd_prompt_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_
  *  tree_mask    [T][mask_words] 32-bit words (device, contiguous), 1 <= mask_words <= 8.
  *  out, lse     as in fd_prompt_attention.
  * v must be finite at a request's keys [0, prefix + tree_len); what stands behind may be anything.
+ * Weights are rounded as in fd_prompt_attention.
  * T and S_cap are at most 2^31 - 1024.
  */
 fd_status fd_tree_attention(const fd_tensor* q, const fd_tensor* k_cache, const fd_tensor* v_cache,
@@ -396,8 +400,9 @@ size_t fd_tree_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_q_
  *  cache_lens       [batch] int32.
  * New pages are taken lowest index first, in the order of the sequences (of the pairs, in
  * fd_pages_fork), so that results are reproducible. batch and the lists' counts are at most 4096.
- * The calls are asynchronous, take no host copy of any of this state, and may be captured. Two calls
- * on the same state must be ordered by the caller.
+ * The calls are asynchronous, take no host copy of any of this state, and may be captured (any
+ * fd_reserve_workspace of the stream before is enough for them). Two calls on the same state must be
+ * ordered by the caller.
  * Flags raised (fd_poll_status): FD_FLAG_BAD_PAGE for an entry outside the pool or a page whose
  * references do not allow the call, FD_FLAG_BAD_INDEX for a sequence index or a keep list that is
  * not valid, FD_FLAG_POOL_FULL when pages ran out, FD_FLAG_LEN_CLAMPED for lengths beyond a row's
@@ -426,7 +431,8 @@ fd_status fd_pages_append(const fd_tensor* k_new, const fd_tensor* v_new, fd_ten
 
 /* fd_pages_append into FD_E4M3 pages: k_new, v_new are FD_BF16 or FD_F32, and the code of x is the
  * E4M3 value nearest to x / scale (ties to even; beyond +-448, infinities included, the code of
- * +-448; NaN gives a NaN code). k_scale, v_scale finite, > 0. */
+ * +-448; NaN gives a NaN code). k_scale, v_scale finite, > 0. The fd_decode_attention_*fp8 calls read
+ * pages of D 128; E4M3 pages of D 64 have no reader in this library. */
 fd_status fd_pages_append_fp8(const fd_tensor* k_new, const fd_tensor* v_new, fd_tensor* k_pages,
                               fd_tensor* v_pages, float k_scale, float v_scale,
                               const int32_t* block_table, int32_t pages_per_seq, int32_t batch,
