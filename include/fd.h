@@ -329,7 +329,8 @@ fd_status fd_decode_attention_static(const fd_tensor* q, const fd_tensor* k_cach
  *  out       [T, Hq, D]   FD_BF16 (written); lse [T, Hq] float32 (contiguous, written, natural
  *            log).
  * v must be finite in the rows of a request (a non-finite value may reach the request's other
- * rows); other rows may hold anything. out must not overlap q, k or v.
+ * rows); other rows may hold anything. out must not overlap q, k or v, nor its rows and heads each
+ * other (a stride of 0 is refused; in q, k and v it is a broadcast).
  * The weights are rounded to one bf16 term for the product with v (the decode and chunk calls keep
  * two): beside its own rounding, out is off by up to 2^-8 of sum_j p_j |v_j| / sum_j p_j. Sums and lse
  * are fp32.
@@ -392,7 +393,8 @@ size_t fd_tree_workspace_bytes(int32_t batch, int32_t total_rows, int32_t num_q_
  * FlashDecoding page, "部署落地的工程细节", pairs split-KV decoding with a paged cache and names no
  * layout; these calls keep the block-table form of fd_decode_attention_paged. All of its state is
  * the caller's device memory:
- *  k_pages, v_pages [num_pages, Hkv, page_size, D] as in fd_decode_attention_paged;
+ *  k_pages, v_pages [num_pages, Hkv, page_size, D] as in fd_decode_attention_paged (a stride of 0 is
+ *                   refused: pages and heads are written);
  *  block_table      [batch][pages_per_seq] int32: the pages of a sequence are the leading
  *                   non-negative entries of its row (what stands behind the first negative entry
  *                   is ignored); an empty row starts with a negative entry;

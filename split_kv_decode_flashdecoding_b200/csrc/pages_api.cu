@@ -28,6 +28,8 @@ fd_status check_pool(const fd_tensor* k, const fd_tensor* v) {
   if (!(psz == 8 || psz == 16 || psz == 32 || psz == 64 || (psz >= 128 && psz % 128 == 0)))
     return fail(FD_ERR_UNSUPPORTED, "page size %lld: must be 8, 16, 32, 64 or a multiple of 128", (long long)psz);
   if (k->stride[2] != d) return fail(FD_ERR_UNSUPPORTED, "token rows of a page must be contiguous (stride[2] == head_dim)");
+  if ((k->shape[0] > 1 && k->stride[0] == 0) || (k->shape[1] > 1 && k->stride[1] == 0))
+    return fail(FD_ERR_UNSUPPORTED, "pages and their heads must not share memory");
   if (!k->data || !v->data) return fail(FD_ERR_INVALID_ARGUMENT, "k_pages / v_pages data is NULL");
   if (!aligned16(k->data) || !aligned16(v->data) || !stride16(k->stride[0], k->dtype) || !stride16(k->stride[1], k->dtype))
     return fail(FD_ERR_UNSUPPORTED, "page data and strides must be 16-byte aligned");

@@ -40,6 +40,8 @@ fd_status resolve_rows(const fd_tensor* q, const fd_tensor* out, int64_t hkv, in
   if (hq / hkv > 16) return fail(FD_ERR_UNSUPPORTED, "group size %lld above 16", (long long)(hq / hkv));
   if (rows > kMaxKeys) return fail(FD_ERR_UNSUPPORTED, "more than 2^31 - 1024 rows");
   if (hq > 65535) return fail(FD_ERR_UNSUPPORTED, "more than 65535 query heads");
+  if ((rows > 1 && out->stride[0] == 0) || (hq > 1 && out->stride[1] == 0))
+    return fail(FD_ERR_UNSUPPORTED, "out's rows and heads must not share memory");
   if (batch < 0) return fail(FD_ERR_INVALID_ARGUMENT, "batch must be >= 0");
   if (batch > kMaxPlanBatch) return fail(FD_ERR_UNSUPPORTED, "batch %d exceeds %d", batch, kMaxPlanBatch);
   p->q = q->data;
